@@ -579,6 +579,232 @@ pld_status pld_draft_control_batch(pld_ctx *ctx, const int32_t *const *histories
                                    double *out_rates, hipStream_t stream);
 
 /*
+ * The verify step: what a target model does with the drafted block.
+ *
+ * The HyperQwen lookup-drafting page (step 2) verifies a 16-token block in
+ * one pass of the target model, at about 1 ms of attention per extra
+ * position at 25k context, and keeps sampling lossless (step 3) by giving
+ * the rejection sampler a point mass at lookup positions. The calls below
+ * are that pass's operators on the buffers the draft calls leave on the
+ * device: rotary positions and the paged cache (pld_kv_append), attention
+ * of the block over the cache (pld_attend), acceptance and the draw of the
+ * token after the accepted ones (pld_verify, whose outputs are pld_append's
+ * tokens and counts and pld_fuse's and pld_control's accepted counts).
+ *
+ * A request's block. lengths[b] = L is the request's history length (the
+ * store's lengths, pld_histories); draft_len[b] = d its draft tokens
+ * (out_len of a draft call, out_positions of pld_fuse). The block has
+ * n = 1 + d rows: row 0 is the history's last token, at position L - 1, and
+ * row t >= 1 is draft token t - 1, at position L - 1 + t. d = 0 is the
+ * single-token step; a prompt goes into the cache as a block of many rows.
+ * A request with L = 0 or d = -1 has no rows: nothing of it is read or
+ * written. Blocks lie in buffers padded to `rows` rows per request; rows
+ * n..rows-1 are neither read nor written.
+ *
+ * Bad inputs seen on the device set the sticky flag: L < 0, d < -1 and
+ * d >= rows as PLD_EINVAL, L + d > max_len as PLD_ECAPACITY. Such a request
+ * has no rows in pld_kv_append; pld_attend writes NaN in all of its `rows`
+ * rows; pld_verify commits nothing (its contract).
+ */
+
+/* element types */
+#define PLD_F32 0
+#define PLD_F16 1
+#define PLD_BF16 2
+#define PLD_E4M3 3 /* 8-bit float, 4 exponent bits, largest 448, no infinity */
+
+/* Rotary positions: what the angles' frequencies are scaled by for long
+   contexts. */
+#define PLD_ROPE_PLAIN 0  /* f_i = base^(-2i / rot_dim) */
+#define PLD_ROPE_LINEAR 1 /* f_i / factor */
+#define PLD_ROPE_BANDED 2 /* by wavelength (YaRN): f_i / factor for the slow
+                             pairs, f_i for the fast ones, a linear ramp
+                             between them */
+
+typedef struct pld_rope_params {
+    int32_t rot_dim;      /* leading dims of a head that rotate: even, 0 (none)
+                             .. head_dim */
+    int32_t interleaved;  /* pairs: 0 = (i, i + rot_dim / 2), 1 = (2i, 2i + 1) */
+    int32_t scaling;      /* PLD_ROPE_* */
+    int32_t original_len; /* banded: the context length trained on, >= 1 */
+    double base;          /* > 1; 10000 */
+    double factor;        /* linear, banded: > 0; 1 */
+    double beta_fast;     /* banded: a pair that turns more often than this in
+                             original_len keeps f_i; 32 */
+    double beta_slow;     /* banded: one that turns less often than this gets
+                             f_i / factor; 1 */
+    double magnitude;     /* factor on the rotated values, > 0; 1 */
+} pld_rope_params;
+
+typedef struct pld_target_params {
+    int32_t max_batch;   /* requests a call may hold, >= 1 */
+    int32_t max_rows;    /* rows of a padded block, >= 1 */
+    int64_t max_len;     /* largest L + d, as pld_create's max_len */
+    int32_t q_heads;     /* a multiple of kv_heads; 0 with kv_heads 0: a context
+                            for pld_verify alone */
+    int32_t kv_heads;
+    int32_t head_dim;    /* 64, 96, 128, 192 or 256 */
+    int32_t dtype;       /* q, k, v and outputs: PLD_F16 or PLD_BF16 */
+    int32_t cache_dtype; /* the cache: dtype or PLD_E4M3 */
+    int32_t page_tokens; /* 16, 32, 64, 128 or 256 */
+    int32_t vocab;       /* of pld_verify; 0: a context without it */
+    pld_rope_params rope;
+} pld_target_params;
+
+/* max_batch 1, max_rows 16, max_len 32768, no heads, head_dim 128, bf16
+   throughout, pages of 64 tokens, vocab 0; rope: rot_dim 0, plain, and the
+   values named in its comments (original_len 32768). Errors: PLD_EINVAL. */
+pld_status pld_target_params_default(pld_target_params *params);
+
+/*
+ * A context for the verify step's calls, holding their workspaces (partial
+ * results of an attention split over the cache, row statistics of a
+ * verification) and the rotary frequencies of params->rope in 64 bits. It
+ * is a context without a store otherwise (pld_sync, pld_destroy and the
+ * draft calls take it). One context serves every layer of a model in turn;
+ * calls that overlap in time need contexts of their own (see the top), and
+ * so do captured graphs that may run at the same time.
+ *  stream: as in pld_create.
+ * Errors: PLD_EINVAL (null, a field outside its range), PLD_ENOMEM, PLD_EHIP.
+ */
+pld_status pld_create_target(pld_ctx **out, const pld_target_params *params,
+                             hipStream_t stream);
+
+/*
+ * The paged cache. A page holds page_tokens positions of one request for all
+ * kv heads; position i of request b lies in page
+ * page_table[b * table_stride + i / page_tokens], slot i % page_tokens.
+ *  k_cache: device cache_dtype [n_pages][kv_heads][page_tokens][head_dim]
+ *  v_cache: device cache_dtype [n_pages][kv_heads][head_dim][page_tokens]
+ * both 16-byte aligned. V lies with its positions side by side: the matrix
+ * instructions that sum probabilities times V take it as it is loaded.
+ *  k_scale, v_scale: device float[kv_heads] or NULL (1): with an E4M3 cache a
+ *  cell holds value / scale, rounded, at most 448 in magnitude. Not used
+ *  with a 16-bit cache.
+ * table_stride >= 1 is also the number of entries a table row holds. A page id
+ * outside [0, n_pages), or a position past its row's entries, is a bad page and
+ * sets the sticky flag (PLD_EINVAL).
+ */
+
+/*
+ * Rotary positions, and the block's keys and values into the cache.
+ *
+ * For every row t < n of every request, at position p = L - 1 + t: the first
+ * rot_dim dims of each q and k head are rotated pair by pair,
+ *   (x, y) -> magnitude * (x cos(p f_i) - y sin(p f_i),
+ *                          x sin(p f_i) + y cos(p f_i)),
+ * the angle reduced in 64 bits, the products in 32, rounded once. q goes to
+ * out_q, k and v to their cell of the cache. Cells of other positions are
+ * left as they are.
+ *  q:     device dtype; row r = b * rows + t at q + r * q_stride, its heads
+ *         side by side (q_heads * head_dim). NULL: no q (out_q NULL too).
+ *  k, v:  the same with kv_stride and kv_heads; q, k and v may be slices of
+ *         one projection's output.
+ *  rows:  1 <= rows <= max_rows.
+ *  batch: 0 <= batch <= max_batch; 0 is a no-op.
+ *  out_q: device dtype [batch * rows][q_heads * head_dim], dense. It may be q
+ *         itself when q_stride is q_heads * head_dim.
+ * Strides are in elements, >= the row's width; q, k, v and out_q need the
+ * alignment of an element only (16 bytes with strides of 8 elements is the
+ * fast case).
+ * A row whose page is bad stores no k and v. Two requests whose tables
+ * give the same cell race for it.
+ * Errors: PLD_EINVAL, PLD_EHIP.
+ */
+pld_status pld_kv_append(pld_ctx *ctx, const void *q, int64_t q_stride, const void *k,
+                         const void *v, int64_t kv_stride, int32_t rows,
+                         const int32_t *lengths, const int32_t *draft_len, int32_t batch,
+                         const int32_t *page_table, int64_t table_stride, void *k_cache,
+                         void *v_cache, int64_t n_pages, const float *k_scale,
+                         const float *v_scale, void *out_q, hipStream_t stream);
+
+/*
+ * Attention of every block's rows over the paged cache, which holds the
+ * rows' own keys and values already (pld_kv_append).
+ *
+ * Row t (position p = L - 1 + t), query head h, kv head h / (q_heads /
+ * kv_heads): s_j = scale * q . k_j over the positions j with
+ * max(0, p - window + 1) <= j <= p (window 0: all up to p);
+ * out = sum_j softmax(s)_j v_j, out_lse = ln sum_j exp(s_j). Scores,
+ * statistics and sums are held in 32 bits; a probability is rounded to dtype
+ * when it meets V in a matrix instruction. Cells past a request's last row
+ * are not used, whatever they hold.
+ *  q, q_stride, rows, lengths, draft_len, batch: as in pld_kv_append; q must be
+ *            16-byte aligned and q_stride a multiple of 8 elements.
+ *  max_len:  host bound on every L + d, 1 <= max_len <= the context's; it sizes
+ *            the launch (0: the context's). A request above it is written as
+ *            NaN and sets the sticky flag (PLD_ECAPACITY).
+ *  scale:    0 means 1 / sqrt(head_dim).
+ *  window:   >= 0.
+ *  out:      device dtype [batch * rows][q_heads * head_dim], dense.
+ *  out_lse:  device float [batch * rows][q_heads] or NULL.
+ * A row that sees a bad page is written as NaN. Results do not depend on timing.
+ * Errors: PLD_EINVAL, PLD_EHIP.
+ */
+pld_status pld_attend(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t rows,
+                      const int32_t *lengths, const int32_t *draft_len, int64_t max_len,
+                      int32_t batch, const int32_t *page_table, int64_t table_stride,
+                      const void *k_cache, const void *v_cache, int64_t n_pages,
+                      const float *k_scale, const float *v_scale, float scale, int32_t window,
+                      void *out, float *out_lse, hipStream_t stream);
+
+/*
+ * Verification of the drafted tokens against the target model's logits, from
+ * given random numbers.
+ *
+ * Row t's logits z_t give p_t = softmax(z_t / T) for the token after row t,
+ * with the request's temperature T. Draft token x_t (t < d) is accepted when
+ *   u_t * q_t(x_t) < p_t(x_t),
+ * q_t(x) the drafter's probability where the position has one, else 1 (a
+ * point mass, lookup positions). Up to the first refusal, at row a, tokens
+ * are committed as drafted; then one token is drawn:
+ *   refused at a point mass: from p_a with x_a left out;
+ *   refused at a position with q: from max(p_a - q_a, 0) (from p_a if that is
+ *     zero throughout);
+ *   nothing refused (a = d): from p_d.
+ * The draw is the first token i, in index order, whose running sum of weights
+ * exceeds u times their total, in 64 bits. This commits tokens distributed
+ * as the target's own samples (the page's lossless verification). T = 0 is
+ * greedy: a draft token is accepted when it is its row's argmax (lowest index
+ * on a tie) and the argmax of row a is committed; u and q are not used.
+ *
+ *  logits:   device logits_dtype (PLD_F32, PLD_F16, PLD_BF16); row r = b * rows
+ *            + t at logits + r * logits_stride, logits_stride >= vocab. -inf
+ *            is a token of probability 0.
+ *  rows:     1 <= rows <= max_rows.
+ *  draft:    device int32 [batch][rows - 1]: a draft call's out_draft with
+ *            k_max = rows - 1, or pld_fuse's out_block (NULL when rows = 1).
+ *  draft_len: device int32[batch], d in [-1, rows - 1].
+ *  src:      device uint64[batch] or NULL: bit t set makes position t a point
+ *            mass whatever draft_probs holds (pld_fuse's out_src; positions
+ *            from 64 on have no bit).
+ *  draft_probs, head: device float [batch][head][vocab], the drafter's
+ *            probabilities at positions 0..head-1, or NULL with head 0;
+ *            0 <= head <= rows - 1.
+ *  temperature: device float[batch], >= 0 and finite, or NULL: 1 throughout.
+ *  uniform:  device float [batch][rows], values in [0, 1): column t < rows - 1
+ *            decides draft position t, the last column draws the token.
+ *  out_tokens: device int32 [batch][rows]: the committed tokens, -1 past them
+ *            (pld_append's tokens with tokens_stride = rows).
+ *  out_accepted: device int32[batch], a: pld_fuse's and pld_control's accepted.
+ *  out_counts: device int32[batch], a + 1: pld_append's counts.
+ *  out_logprobs: device float [batch][rows] or NULL: ln p_t of each committed
+ *            token (at T = 1 for greedy requests), 0 past them.
+ * d = -1: no tokens, a = 0 and count 0. Rows after a refusal need not be
+ * read and are not checked. A request is written like d = -1 and sets the
+ * sticky flag (PLD_EINVAL) when d is outside its range, a draft token before d
+ * outside the vocabulary, T negative or not finite, a uniform it may use
+ * outside [0, 1), or a row it needs holds NaN, +inf or only -inf.
+ * Errors: PLD_EINVAL, PLD_EHIP.
+ */
+pld_status pld_verify(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
+                      int64_t logits_stride, int32_t rows, const int32_t *draft,
+                      const int32_t *draft_len, const uint64_t *src, const float *draft_probs,
+                      int32_t head, const float *temperature, const float *uniform,
+                      int32_t batch, int32_t *out_tokens, int32_t *out_accepted,
+                      int32_t *out_counts, float *out_logprobs, hipStream_t stream);
+
+/*
  * Wait for the device (the given stream and every other stream), then
  * report and clear the sticky device-side flag. The flag exists so that a
  * bad request is reported and never silently cut short (the Strata engine
@@ -587,8 +813,10 @@ pld_status pld_draft_control_batch(pld_ctx *ctx, const int32_t *const *histories
  * PLD_OK when clear; PLD_ECAPACITY when a history exceeded max_len (or its
  * row's stride) or an append overflowed; PLD_EINVAL when a length or count
  * was negative, a length was below a strided call's min_len, a row pointer
- * was null or misaligned, pld_fuse saw inconsistent per-request inputs, or
- * pld_control an outcome out of range (capacity wins when both are set).
+ * was null or misaligned, pld_fuse saw inconsistent per-request inputs,
+ * pld_control an outcome out of range, or a verify-step call a bad block,
+ * page id, token, temperature, random number or logit (capacity wins when
+ * both are set).
  * Errors: PLD_EINVAL (null ctx), PLD_EHIP.
  */
 pld_status pld_sync(pld_ctx *ctx, hipStream_t stream);

@@ -36,6 +36,8 @@ EXPORTS = ("pld_create", "pld_create_indexed", "pld_destroy", "pld_configure", "
            "pld_fuse", "pld_draft_fuse_batch", "pld_control_params_default", "pld_control",
            "pld_ngram_params_default", "pld_create_ngram", "pld_draft_ngram",
            "pld_append_draft_ngram", "pld_draft_control_batch",
+           "pld_target_params_default", "pld_create_target", "pld_kv_append", "pld_attend",
+           "pld_verify",
            "pld_sync", "pld_strerror",
            "pld_last_error")
 
@@ -71,6 +73,40 @@ class PldNgramParams(ctypes.Structure):
     _fields_ = [("n_min", ctypes.c_int32), ("n_max", ctypes.c_int32),
                 ("min_count", ctypes.c_int32 * PLD_NGRAM_MAX_N),
                 ("min_percent", ctypes.c_int32 * PLD_NGRAM_MAX_N)]
+
+
+PLD_F32, PLD_F16, PLD_BF16, PLD_E4M3 = 0, 1, 2, 3
+PLD_ROPE_PLAIN, PLD_ROPE_LINEAR, PLD_ROPE_BANDED = 0, 1, 2
+
+
+class PldRopeParams(ctypes.Structure):
+    """pld_rope_params (include/pld.h): rotary positions of a target model."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("original_len", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class PldTargetParams(ctypes.Structure):
+    """pld_target_params (include/pld.h): the geometry of the verify step's
+    calls; pld_target_params_default() gives the defaults."""
+    _fields_ = [("max_batch", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("max_len", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("cache_dtype", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("rope", PldRopeParams)]
+
+
+def __getattr__(name):
+    # PLD_TYPES: the torch dtype of every element type (torch is imported
+    # only where a call needs it)
+    if name == "PLD_TYPES":
+        import torch
+        return {torch.float32: PLD_F32, torch.float16: PLD_F16, torch.bfloat16: PLD_BF16,
+                torch.float8_e4m3fn: PLD_E4M3}
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class PldError(RuntimeError):
@@ -121,6 +157,14 @@ def load(path: str = LIB_PATH):
                                    vp, vp, vp, vp],
         "pld_draft_control_batch": [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp,
                                     ctypes.POINTER(PldControlParams), vp, vp, vp, vp, vp, vp],
+        "pld_target_params_default": [ctypes.POINTER(PldTargetParams)],
+        "pld_create_target": [ctypes.POINTER(vp), ctypes.POINTER(PldTargetParams), vp],
+        "pld_kv_append": [vp, vp, i64, vp, vp, i64, i32, vp, vp, i32, vp, i64, vp, vp, i64, vp,
+                          vp, vp, vp],
+        "pld_attend": [vp, vp, i64, i32, vp, vp, i64, i32, vp, i64, vp, vp, i64, vp, vp,
+                       ctypes.c_float, i32, vp, vp, vp],
+        "pld_verify": [vp, vp, i32, i64, i32, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp,
+                       vp],
         "pld_sync": [vp, vp],
     }
     for name, args in sig.items():
@@ -452,6 +496,128 @@ def pld_append_draft_ngram(ctx: int, tokens, tokens_stride: int, counts, batch: 
         ctx, _dev_ptr(tokens, "tokens", i32), int(tokens_stride), _dev_ptr(counts, "counts", i32),
         int(batch), ctypes.byref(params), int(k_max), _dev_ptr(out_draft, "out_draft", i32),
         _dev_ptr(out_len, "out_len", i32), _dev_ptr(out_levels, "out_levels", i32),
+        _stream(stream)))
+
+
+def _rows_ptr(x, name: str, dtypes):
+    """Device pointer of rows at a stride: a GPU tensor (or a slice of one)
+    whose last dimension is dense, of one of `dtypes`; or a raw pointer."""
+    if x is None:
+        return 0
+    if isinstance(x, int):
+        return x
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor or a device pointer")
+    if x.device.type != "cuda":
+        raise ValueError(f"{name}: tensor must be on the GPU (got {x.device})")
+    if x.numel() and x.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense (stride {x.stride(-1)})")
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype must be one of {tuple(dtypes)} (got {x.dtype})")
+    return x.data_ptr()
+
+
+def _same_device(**tensors) -> None:
+    """Every tensor lies on the current device, whose stream the call takes."""
+    import torch
+    current = None
+    for name, x in tensors.items():
+        if isinstance(x, torch.Tensor) and x.device.type == "cuda":
+            if current is None:
+                current = torch.cuda.current_device()
+            if x.device.index != current:
+                raise ValueError(f"{name}: tensor is on {x.device}, the current device is "
+                                 f"cuda:{current}")
+
+
+def pld_target_params_default() -> PldTargetParams:
+    p = PldTargetParams()
+    _check("pld_target_params_default", load().pld_target_params_default(ctypes.byref(p)))
+    return p
+
+
+def pld_create_target(params: PldTargetParams, stream=None) -> int:
+    """A context for the verify step's calls (include/pld.h)."""
+    ctx = ctypes.c_void_p()
+    _check("pld_create_target", load().pld_create_target(
+        ctypes.byref(ctx), ctypes.byref(params), _create_stream(stream)))
+    return ctx.value
+
+
+def pld_kv_append(ctx: int, q, q_stride: int, k, v, kv_stride: int, rows: int, lengths,
+                  draft_len, batch: int, page_table, table_stride: int, k_cache, v_cache,
+                  n_pages: int, k_scale=None, v_scale=None, out_q=None, stream=None) -> None:
+    """Rotary positions, and the block's keys and values into the paged
+    cache (include/pld.h). q, k and v may be slices whose rows lie q_stride
+    and kv_stride elements apart."""
+    import torch
+    i32, half = _i32(), (torch.float16, torch.bfloat16)
+    cell = half + (torch.float8_e4m3fn,)
+    _same_device(q=q, k=k, v=v, lengths=lengths, draft_len=draft_len, page_table=page_table,
+                 k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out_q=out_q)
+    _check("pld_kv_append", load().pld_kv_append(
+        ctx, _rows_ptr(q, "q", half), int(q_stride), _rows_ptr(k, "k", half),
+        _rows_ptr(v, "v", half), int(kv_stride), int(rows), _dev_ptr(lengths, "lengths", i32),
+        _dev_ptr(draft_len, "draft_len", i32), int(batch),
+        _dev_ptr(page_table, "page_table", i32), int(table_stride),
+        _cells(k_cache, "k_cache", cell), _cells(v_cache, "v_cache", cell), int(n_pages),
+        _dev_ptr(k_scale, "k_scale", torch.float32), _dev_ptr(v_scale, "v_scale", torch.float32),
+        _cells(out_q, "out_q", half), _stream(stream)))
+
+
+def _cells(x, name: str, dtypes) -> int:
+    """_dev_ptr of a contiguous buffer of one of `dtypes`."""
+    if x is not None and not isinstance(x, int) and getattr(x, "dtype", None) not in dtypes:
+        raise ValueError(f"{name}: dtype must be one of {tuple(dtypes)}")
+    return _dev_ptr(x, name)
+
+
+def pld_attend(ctx: int, q, q_stride: int, rows: int, lengths, draft_len, max_len: int,
+               batch: int, page_table, table_stride: int, k_cache, v_cache, n_pages: int,
+               k_scale=None, v_scale=None, scale: float = 0.0, window: int = 0, out=None,
+               out_lse=None, stream=None) -> None:
+    """Attention of the block's rows over the paged cache (include/pld.h)."""
+    import torch
+    i32, half = _i32(), (torch.float16, torch.bfloat16)
+    cell = half + (torch.float8_e4m3fn,)
+    _same_device(q=q, lengths=lengths, draft_len=draft_len, page_table=page_table,
+                 k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=out,
+                 out_lse=out_lse)
+    _check("pld_attend", load().pld_attend(
+        ctx, _rows_ptr(q, "q", half), int(q_stride), int(rows),
+        _dev_ptr(lengths, "lengths", i32), _dev_ptr(draft_len, "draft_len", i32), int(max_len),
+        int(batch), _dev_ptr(page_table, "page_table", i32), int(table_stride),
+        _cells(k_cache, "k_cache", cell), _cells(v_cache, "v_cache", cell), int(n_pages),
+        _dev_ptr(k_scale, "k_scale", torch.float32), _dev_ptr(v_scale, "v_scale", torch.float32),
+        float(scale), int(window), _cells(out, "out", half),
+        _dev_ptr(out_lse, "out_lse", torch.float32), _stream(stream)))
+
+
+def pld_verify(ctx: int, logits, logits_stride: int, rows: int, draft, draft_len, src,
+               draft_probs, head: int, temperature, uniform, batch: int, out_tokens,
+               out_accepted, out_counts, out_logprobs=None, stream=None) -> None:
+    """Verification of drafted tokens (include/pld.h). `logits` is a tensor
+    (or a slice of one) whose rows lie logits_stride elements apart; its
+    dtype is the call's logits_dtype. `src` is an int64 tensor of bit masks
+    or None, `temperature` a float32 tensor or None (1 throughout)."""
+    import torch
+    i32, f32 = _i32(), torch.float32
+    types = {torch.float32: PLD_F32, torch.float16: PLD_F16, torch.bfloat16: PLD_BF16}
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits: expected a torch tensor")
+    _same_device(logits=logits, draft=draft, draft_len=draft_len, src=src,
+                 draft_probs=draft_probs, temperature=temperature, uniform=uniform,
+                 out_tokens=out_tokens, out_accepted=out_accepted, out_counts=out_counts,
+                 out_logprobs=out_logprobs)
+    ptr = _rows_ptr(logits, "logits", types)
+    _check("pld_verify", load().pld_verify(
+        ctx, ptr, types[logits.dtype], int(logits_stride), int(rows),
+        _dev_ptr(draft, "draft", i32), _dev_ptr(draft_len, "draft_len", i32),
+        _dev_ptr(src, "src", torch.int64), _dev_ptr(draft_probs, "draft_probs", f32), int(head),
+        _dev_ptr(temperature, "temperature", f32), _dev_ptr(uniform, "uniform", f32), int(batch),
+        _dev_ptr(out_tokens, "out_tokens", i32), _dev_ptr(out_accepted, "out_accepted", i32),
+        _dev_ptr(out_counts, "out_counts", i32), _dev_ptr(out_logprobs, "out_logprobs", f32),
         _stream(stream)))
 
 

@@ -36,6 +36,8 @@ SOURCE_FLAGS = {"pld_kernels.hip": ["-mllvm", "-amdgpu-atomic-optimizer-strategy
 def sources():
     return [os.path.join(CSRC, "pld_kernels.hip"), os.path.join(CSRC, "pld_index.hip"),
             os.path.join(CSRC, "pld_control.hip"), os.path.join(CSRC, "pld_ngram.hip"),
+            os.path.join(CSRC, "pld_kv.hip"), os.path.join(CSRC, "pld_attend.hip"),
+            os.path.join(CSRC, "pld_verify.hip"), os.path.join(CSRC, "pld_target_api.cpp"),
             os.path.join(CSRC, "pld_api.cpp")]
 
 

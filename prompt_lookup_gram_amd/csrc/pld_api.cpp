@@ -12,38 +12,17 @@
 #include <hip/hip_runtime_api.h>
 
 #include "pld.h"
+#include "pld_ctx.h"
 #include "pld_kernels.h"
-
-struct pld_ctx {
-    int device;
-    int32_t max_batch;
-    int32_t max_len;
-    int32_t tile_tokens;        // scan tile size; 0: chosen per call (pick_tile)
-    int32_t fused;
-    pld::ReqSlot *slots;        // [max_batch] reduction state
-    unsigned int *err;          // one word
-    int4 *zero16;               // 16 zero bytes
-    int32_t *store;             // [max_batch * pitch] or null
-    int64_t pitch;              // tokens per store row
-    int32_t *store_len;         // [max_batch] or null
-    const int32_t **store_rows; // [max_batch] device row pointers or null
-    unsigned long long *index;  // n-gram index over the store, or null
-    int64_t index_cap;          // slots per (request, length) table
-    int32_t index_lo, index_hi; // indexed lengths
-    int32_t index_chunks;       // workgroups per request for an append's inserts
-    uint32_t index_fp_mask;     // fingerprint bits kept
-    unsigned long long *ngram_grams;  // successor-count cache: gram slots, or null
-    unsigned long long *ngram_pairs;  // and pair slots
-    int64_t ngram_cap;                // slots per (request, length) table
-    int32_t ngram_n_max;              // context lengths 1..ngram_n_max
-    int32_t ngram_chunks;             // workgroups per request for a large append
-};
+#include "pld_target.h"
 
 namespace {
 
 thread_local char g_last_error[256] = "";
 
-pld_status fail(pld_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+namespace pld {
 
 pld_status fail(pld_status s, const char *fmt, ...)
 {
@@ -59,6 +38,13 @@ pld_status hip_fail(hipError_t e, const char *what)
     return fail(PLD_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+}  // namespace pld
+
+using pld::fail;
+using pld::hip_fail;
+
+namespace {
+
 void release(pld_ctx *c)
 {
     if (!c)
@@ -72,6 +58,7 @@ void release(pld_ctx *c)
     if (c->index) (void)hipFree(c->index);
     if (c->ngram_grams) (void)hipFree(c->ngram_grams);
     if (c->ngram_pairs) (void)hipFree(c->ngram_pairs);
+    if (c->target) pld::target_release(c->target);
     delete c;
 }
 
@@ -1028,7 +1015,7 @@ pld_status pld_sync(pld_ctx *ctx, hipStream_t stream)
     // every problem read in this call is named; capacity wins the status
     const pld_status st =
         (bits & (pld::kErrLenCapacity | pld::kErrAppendCapacity)) ? PLD_ECAPACITY : PLD_EINVAL;
-    return fail(st, "device reported:%s%s%s%s%s%s%s%s",
+    return fail(st, "device reported:%s%s%s%s%s%s%s%s%s%s",
                 (bits & pld::kErrLenCapacity) ? " a history longer than max_len;" : "",
                 (bits & pld::kErrAppendCapacity) ? " an append past max_len;" : "",
                 (bits & pld::kErrLenNegative) ? " a negative length;" : "",
@@ -1036,7 +1023,9 @@ pld_status pld_sync(pld_ctx *ctx, hipStream_t stream)
                 (bits & pld::kErrAppendNegative) ? " a negative append count;" : "",
                 (bits & pld::kErrBelowMinLen) ? " a length below the promised min_len;" : "",
                 (bits & pld::kErrFuseInput) ? " inconsistent fusion inputs;" : "",
-                (bits & pld::kErrControlInput) ? " a controller outcome out of range;" : "");
+                (bits & pld::kErrControlInput) ? " a controller outcome out of range;" : "",
+                (bits & pld::kErrBlock) ? " a bad verify block input;" : "",
+                (bits & pld::kErrPage) ? " a page id outside the cache;" : "");
 }
 
 const char *pld_strerror(pld_status status)

@@ -21,7 +21,9 @@ enum : uint32_t {
     kErrAppendNegative = 16u, // counts[b] < 0
     kErrBelowMinLen = 32u,    // strided batch: lengths[b] < the caller's min_len
     kErrFuseInput = 64u,      // pld_fuse: inconsistent per-request inputs
-    kErrControlInput = 128u   // pld_control: an outcome or lookup input out of range
+    kErrControlInput = 128u,  // pld_control: an outcome or lookup input out of range
+    kErrBlock = 256u,         // verify step: draft_len, token, temperature, uniform or logits
+    kErrPage = 512u           // verify step: a page id outside the cache
 };
 
 // Per-request reduction state of the fused gather: the packed key maximum
