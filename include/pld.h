@@ -738,7 +738,8 @@ pld_status pld_kv_append(pld_ctx *ctx, const void *q, int64_t q_stride, const vo
  *  window:   >= 0.
  *  out:      device dtype [batch * rows][q_heads * head_dim], dense.
  *  out_lse:  device float [batch * rows][q_heads] or NULL.
- * A row that sees a bad page is written as NaN. Results do not depend on timing.
+ * A row that sees a bad page is written as NaN (other rows of its request may
+ * be, too). Results do not depend on timing.
  * Errors: PLD_EINVAL, PLD_EHIP.
  */
 pld_status pld_attend(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t rows,

@@ -55,6 +55,8 @@ struct AttendArgs {
     int32_t window;            // 0: none
     void *out;
     float *out_lse;            // or null
+    float *ws;                 // workspace: partial results of ws_rows rows
+    int64_t ws_rows;           // (head_dim floats each, then two floats each)
 };
 
 struct VerifyArgs {
@@ -83,10 +85,14 @@ struct Target {
     int32_t page_shift;
     double *turns;       // device [rot_dim / 2]
     void *verify_ws;     // device, when vocab > 0
+    float *attend_ws;    // device, when there are heads
+    int64_t attend_rows;
 };
 
 void target_release(Target *t);
 
+// Rows of partial results pld_attend's workspace should hold.
+int64_t attend_rows(const pld_target_params &p);
 size_t verify_workspace(int32_t batch, int32_t rows, int32_t vocab);
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
 hipError_t launch_attend(const AttendArgs &a, hipStream_t s);

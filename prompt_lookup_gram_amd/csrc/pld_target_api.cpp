@@ -24,6 +24,7 @@ void target_release(Target *t)
 {
     if (t->turns) (void)hipFree(t->turns);
     if (t->verify_ws) (void)hipFree(t->verify_ws);
+    if (t->attend_ws) (void)hipFree(t->attend_ws);
     delete t;
 }
 
@@ -151,8 +152,8 @@ pld_status block_args(pld_ctx *ctx, int32_t rows, const int32_t *lengths,
     if (max_len < 0 || max_len > p.max_len)
         return fail(PLD_EINVAL, "max_len %lld outside [0, the context's %lld]",
                     (long long)max_len, (long long)p.max_len);
-    if (n_pages < 0 || n_pages > 0x7fffffffLL)
-        return fail(PLD_EINVAL, "n_pages must be in [0, 2^31-1] (got %lld)", (long long)n_pages);
+    if (n_pages < 1 || n_pages > 0x7fffffffLL)
+        return fail(PLD_EINVAL, "n_pages must be in [1, 2^31-1] (got %lld)", (long long)n_pages);
     if (table_stride < 1)
         return fail(PLD_EINVAL, "table_stride must be >= 1 (got %lld)", (long long)table_stride);
     if (batch > 0 && (!lengths || !draft_len || !page_table || !k_cache || !v_cache))
@@ -248,6 +249,11 @@ pld_status pld_create_target(pld_ctx **out, const pld_target_params *params, hip
     if (memory && e == hipSuccess && p.vocab > 0)
         memory = hipMalloc(&t->verify_ws, pld::verify_workspace(p.max_batch, p.max_rows,
                                                                 p.vocab)) == hipSuccess;
+    if (memory && e == hipSuccess && p.q_heads > 0) {
+        t->attend_rows = pld::attend_rows(p);
+        memory = hipMalloc((void **)&t->attend_ws,
+                           (size_t)t->attend_rows * (p.head_dim + 2) * sizeof(float)) == hipSuccess;
+    }
     if (!memory || e != hipSuccess) {
         (void)hipGetLastError();
         (void)pld_destroy(c);
@@ -338,6 +344,8 @@ pld_status pld_attend(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t row
     a.window = window;
     a.out = out;
     a.out_lse = out_lse;
+    a.ws = ctx->target->attend_ws;
+    a.ws_rows = ctx->target->attend_rows;
     const hipError_t e = pld::launch_attend(a, stream);
     if (e != hipSuccess)
         return hip_fail(e, "attention launch");

@@ -238,6 +238,55 @@ def test_a_context_whose_every_score_is_minus_infinity_is_nan():
         B.pld_destroy(ctx)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("value", ["nan", "inf"])
+@pytest.mark.parametrize("hq,hk", [(4, 4), (8, 1)])
+def test_rows_do_not_see_what_is_not_finite_after_or_before_them(cache, value, hq, hk):
+    """A draft position whose k and v overflowed touches the rows from it on
+    only; a position that a window leaves behind touches none after that."""
+    import torch
+    rows = 12
+    c = Case([90, 61, 300], [rows - 1, 7, rows - 1], rows, hq=hq, hk=hk, dim=64, cache=cache,
+             seed=14)
+    window = 40
+    ctx = c.context()
+    try:
+        clean = c.outputs()
+        c.call(ctx, *clean, window)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        # request 0: position of row 5; 1: of row 0; 2: the window's first
+        # position of row 3
+        hit = [89 + 5, 60, 299 + 3 - window + 1]
+        for i, p in enumerate(hit):
+            page = int(c.table[i, p // c.page])
+            x = torch.tensor(float(value)).to(c.vc.dtype)
+            c.vc[page, :, :, p % c.page] = x
+            c.kc[page, :, p % c.page, :] = x
+        out, lse = c.outputs()
+        c.call(ctx, out, lse, window)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        for i in range(3):
+            for t in range(R.block_rows(c.lengths[i], c.dlen[i])):
+                p = c.lengths[i] - 1 + t
+                if p - window < hit[i] <= p:
+                    assert bool(out[i, t].isnan().all()), (i, t)
+                else:
+                    assert torch.equal(out[i, t], clean[0][i, t]), (i, t)
+                    assert torch.equal(lse[i, t], clean[1][i, t]), (i, t)
+        # an infinity in V alone, seen: it carries the row's dims
+        if value == "inf" and cache == "bf16":
+            c.kc.zero_()
+            c.vc.zero_()
+            page = int(c.table[0, 94 // c.page])
+            c.vc[page, :, 3, 94 % c.page] = float("inf")
+            c.call(ctx, out, lse, window)
+            assert B.pld_sync(ctx) == B.PLD_OK
+            assert bool((out[0, :5] == 0).all()) and bool((out[0, 5:, :, 3] == torch.inf).all())
+            assert bool((out[0, 5:, :, 4:] == 0).all())
+    finally:
+        B.pld_destroy(ctx)
+
+
 def test_cache_offsets_past_32_bits():
     import torch
     # 40,000 pages of 8 heads x 64 x 128: 2.6e9 elements a cache; the request
