@@ -76,7 +76,8 @@ struct VerifyArgs {
     int32_t *out_counts;
     float *out_logprobs;       // or null
     unsigned int *err;
-    void *stats;               // workspace: statistics of pieces of rows
+    void *stats;               // workspace, for max_batch blocks of max_rows rows
+    int32_t max_batch, max_rows;
 };
 
 // What pld_create_target adds to a context.
@@ -94,6 +95,8 @@ void target_release(Target *t);
 // Rows of partial results pld_attend's workspace should hold.
 int64_t attend_rows(const pld_target_params &p);
 size_t verify_workspace(int32_t batch, int32_t rows, int32_t vocab);
+// Sets a new workspace's counters.
+hipError_t verify_clear(void *ws, int32_t batch, int32_t rows, int32_t vocab, hipStream_t s);
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
 hipError_t launch_attend(const AttendArgs &a, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t s);

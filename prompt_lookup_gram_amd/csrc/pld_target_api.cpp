@@ -249,6 +249,12 @@ pld_status pld_create_target(pld_ctx **out, const pld_target_params *params, hip
     if (memory && e == hipSuccess && p.vocab > 0)
         memory = hipMalloc(&t->verify_ws, pld::verify_workspace(p.max_batch, p.max_rows,
                                                                 p.vocab)) == hipSuccess;
+    if (memory && e == hipSuccess && p.vocab > 0) {
+        e = pld::verify_clear(t->verify_ws, p.max_batch, p.max_rows, p.vocab, stream);
+        const hipError_t w = hipStreamSynchronize(stream);
+        if (e == hipSuccess)
+            e = w;
+    }
     if (memory && e == hipSuccess && p.q_heads > 0) {
         t->attend_rows = pld::attend_rows(p);
         memory = hipMalloc((void **)&t->attend_ws,
@@ -407,6 +413,8 @@ pld_status pld_verify(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
     a.out_logprobs = out_logprobs;
     a.err = ctx->err;
     a.stats = ctx->target->verify_ws;
+    a.max_batch = p.max_batch;
+    a.max_rows = p.max_rows;
     const hipError_t e = pld::launch_verify(a, stream);
     if (e != hipSuccess)
         return hip_fail(e, "verification launch");

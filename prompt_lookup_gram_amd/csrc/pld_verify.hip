@@ -1,5 +1,28 @@
 // Verification of drafted tokens against the target model's logits, for
 // gfx950 (MI355X).
+//
+// Mathematics. For every row t of a block: top_t = max z, Z_t = sum exp((z -
+// top_t) / T) in one read of the row; the draft token is accepted when u q <
+// exp((z_x - top_t) / T) / Z_t. The row after the accepted ones is read once
+// more, in 64 bits, for the draw: running sums of weights over pieces, then
+// inside the piece that holds u times the total.
+//
+// Bound by reading the rows (2 or 4 bytes a logit, 7.5 vector operations at
+// 16 bits, about the two's balance). Three things follow:
+//  - a piece of a row lives in one workgroup's registers between the maximum
+//    and the sum, so it is read once;
+//  - rows are dispatched in the order of t, and the workgroup that completes
+//    a row decides it; rows after one that is refused are skipped as soon as
+//    that is known (`stop`). What is skipped never changes a result: only
+//    rows up to the first refusal are looked at;
+//  - the 32-bit sum decides only where it is clear. Its relative error is
+//    below 32 * 2^-23 (the arguments' rounding, weighed by the softmax, is at
+//    most ln V * 2^-23 for V < 2^18, the function's and the additions' the
+//    rest), so within 2^-16 of the edge the deciding workgroup sums the row
+//    again in 64 bits.
+// Numbers that cross workgroups do so in relaxed agent-scope atomics, each
+// performed at the point of coherence; a workgroup waits for its stores to
+// complete before it counts itself in, so who counts last reads them all.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -12,219 +35,590 @@ namespace pld {
 namespace {
 
 constexpr int kWave = 64;
-constexpr int kPiece = 4096;      // logits of a row per wavefront
-constexpr int kFinish = 1024;     // threads of the finishing workgroup
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kDraw = 4096;                 // logits of a draw's piece
+constexpr int kPer = kDraw / kThreads;      // of a thread
+constexpr int32_t kNever = 0x7f7f7f7f;      // `stop` before a refusal
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kClear = 1.0 / 65536;      // relative distance that 32 bits decide
 
-// Statistics of a piece of a row: the largest logit, its lowest index, and
-// the sum of exp((z - top) / T). A NaN or +inf in the piece makes the sum NaN.
+// A piece of a row: the largest logit, the sum of exp((z - top) / T) (NaN
+// when it holds NaN or +inf), and the lowest index of the largest (greedy).
 struct Piece {
-    float top;
-    float sum;
-    int32_t arg;
+    unsigned long long top_sum;
+    unsigned long long arg;
 };
+
+enum : int32_t { kAccept = 0, kRefuse = 1, kBad = 2 };
+
+// A row, decided.
+struct Row {
+    double total;
+    float top;
+    float logp;      // of the draft token
+    int32_t arg;     // greedy
+    int32_t verdict;
+    int32_t pad[2];
+};
+
+// The workspace, laid out for `rows` rows and `vocab` logits.
+struct Space {
+    Piece *pieces;      // [batch * rows][pieces]
+    Row *rows;          // [batch * rows]
+    double *weights;    // [batch][draws]: sums of a draw's pieces
+    double *excess;     // [batch][draws]: the same over q
+    int32_t *arrived;   // [batch * rows], 0 between calls
+    int32_t *drawn;     // [batch], 0 between calls
+    int32_t *stop;      // [batch], kNever between calls
+};
+
+constexpr int kMinPiece = 2048;
+
+__host__ __device__ int64_t pieces_of(int32_t vocab, int piece)
+{
+    return ((int64_t)vocab + piece - 1) / piece;
+}
+
+// Offsets by the context's sizes, so that every call of a context agrees.
+__host__ __device__ Space space_of(char *p, int64_t batch, int64_t rows, int32_t vocab,
+                                   size_t *size)
+{
+    Space s;
+    char *const from = p;
+    s.pieces = (Piece *)p;
+    p += batch * rows * pieces_of(vocab, kMinPiece) * sizeof(Piece);
+    s.rows = (Row *)p;
+    p += batch * rows * sizeof(Row);
+    s.weights = (double *)p;
+    p += batch * pieces_of(vocab, kDraw) * sizeof(double);
+    s.excess = (double *)p;
+    p += batch * pieces_of(vocab, kDraw) * sizeof(double);
+    s.arrived = (int32_t *)p;
+    p += batch * rows * sizeof(int32_t);
+    s.drawn = (int32_t *)p;
+    p += batch * sizeof(int32_t);
+    s.stop = (int32_t *)p;
+    p += batch * sizeof(int32_t);
+    if (size)
+        *size = (size_t)(p - from);
+    return s;
+}
+
+template <typename X>
+__device__ __forceinline__ X peek(const X *p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename X>
+__device__ __forceinline__ void poke(X *p, X v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Counts this workgroup in, its stores before it complete; thread 0 only.
+__device__ __forceinline__ int32_t arrive(int32_t *counter)
+{
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    return __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 __device__ __forceinline__ float temperature(const VerifyArgs &a, int32_t b)
 {
     return a.temperature ? a.temperature[b] : 1.0f;
 }
 
-// One wavefront per piece of a row.
-template <typename T>
-__global__ __launch_bounds__(kWave) void stats_kernel(VerifyArgs a)
+__device__ __forceinline__ float wave_max(float x)
 {
-    const int32_t b = blockIdx.z, t = blockIdx.y;
-    if (t > a.draft_len[b])
-        return;
-    const float temp = temperature(a, b);
-    const float c = 1.0f / (temp > 0.0f ? temp : 1.0f);
-    const T *z = (const T *)a.logits + ((int64_t)b * a.rows + t) * a.stride;
-    const int32_t lo = blockIdx.x * kPiece;
-    const int32_t hi = lo + kPiece < a.vocab ? lo + kPiece : a.vocab;
-    float top = -INFINITY;
-    int32_t arg = 0x7fffffff;
-    for (int32_t i = lo + threadIdx.x; i < hi; i += kWave) {
-        const float x = to_f32(z[i]);
-        if (x > top) {
-            top = x;
-            arg = i;
-        }
-    }
-    for (int i = kWave / 2; i; i >>= 1) {
-        const float x = __shfl_xor(top, i);
-        const int32_t k = __shfl_xor(arg, i);
-        if (x > top || (x == top && k < arg)) {
-            top = x;
-            arg = k;
-        }
-    }
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    for (int32_t i = lo + threadIdx.x; i < hi; i += kWave)
-        sum += __expf((to_f32(z[i]) - base) * c);
     for (int i = kWave / 2; i; i >>= 1)
-        sum += __shfl_xor(sum, i);
-    if (threadIdx.x == 0)
-        ((Piece *)a.stats)[((int64_t)b * a.rows + t) * gridDim.x + blockIdx.x] =
-            Piece{top, sum, arg};
+        x = fmaxf(x, __shfl_xor(x, i));
+    return x;
 }
-
-// Sum over the workgroup, the same on every thread.
-__device__ double block_sum(double x, double *lds)
+template <typename X>
+__device__ __forceinline__ X wave_sum(X x)
 {
     for (int i = kWave / 2; i; i >>= 1)
         x += __shfl_xor(x, i);
+    return x;
+}
+
+// Sum over the workgroup, the same on every thread.
+__device__ __forceinline__ double block_sum(double x, double *lds)
+{
+    x = wave_sum(x);
     __syncthreads();
     if (threadIdx.x % kWave == 0)
         lds[threadIdx.x / kWave] = x;
     __syncthreads();
     double s = 0.0;
-    for (int w = 0; w < kFinish / kWave; ++w)
+    for (int w = 0; w < kWaves; ++w)
         s += lds[w];
     return s;
 }
 
-// One workgroup per request: accepts its draft row by row, then draws.
+// 16 bytes of logits at any element's address.
 template <typename T>
-__global__ __launch_bounds__(kFinish) void finish_kernel(VerifyArgs a, int32_t pieces)
+struct __attribute__((packed, aligned(sizeof(T)))) Word {
+    T x[16 / sizeof(T)];
+};
+
+// Whether position t of request b has drafter probabilities.
+__device__ __forceinline__ const float *claim_of(const VerifyArgs &a, int32_t b, int32_t t,
+                                                 int32_t d)
 {
-    __shared__ double lds[kFinish / kWave];
-    __shared__ double run[kFinish];
-    __shared__ int32_t pick, last;
-    const int32_t b = blockIdx.x, tid = threadIdx.x, v = a.vocab;
+    if (t >= d || t >= a.head || (a.src && t < 64 && ((a.src[b] >> t) & 1)))
+        return nullptr;
+    return a.probs + ((int64_t)b * a.head + t) * a.vocab;
+}
+
+// One workgroup per piece of a row, W 16-byte words a thread.
+template <typename T, int W>
+__global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a, Space sp, uint32_t pieces)
+{
+    constexpr int N = 16 / sizeof(T);
+    constexpr int kPiece = W * N * kThreads;
+    __shared__ float lds_max[kWaves], lds_sum[kWaves];
+    __shared__ int32_t lds_arg[kWaves];
+    __shared__ int32_t lds_say;
+    __shared__ float lds_top;
+    __shared__ double lds_d[kWaves];
+    const int32_t piece = blockIdx.x % pieces, tid = threadIdx.x;
+    const uint32_t order = blockIdx.x / pieces;
+    const int32_t b = order % (uint32_t)a.batch, t = order / (uint32_t)a.batch;
+    const int wave = tid / kWave, lane = tid % kWave;
     const int32_t d = a.draft_len[b];
+    if (t > d || d >= a.rows || peek(sp.stop + b) < t)
+        return;
+    const T *z = (const T *)a.logits + ((int64_t)b * a.rows + t) * a.stride;
     const float tf = temperature(a, b);
     const bool greedy = tf == 0.0f;
-    const double inv = greedy ? 1.0 : 1.0 / (double)tf;
-    const float *u = a.uniform + (int64_t)b * a.rows;
-    const int32_t *x = a.draft + (int64_t)b * (a.rows - 1);
-    bool bad = d < -1 || d >= a.rows || !(tf >= 0.0f) || tf == INFINITY;
-    if (!bad && d >= 0) {
-        for (int32_t t = 0; t < d; ++t)
-            bad |= x[t] < 0 || x[t] >= v || (!greedy && !(u[t] >= 0.0f && u[t] < 1.0f));
-        bad |= !greedy && !(u[a.rows - 1] >= 0.0f && u[a.rows - 1] < 1.0f);
-    }
-    int32_t accepted = 0, token = -1;
-    for (int32_t t = 0; !bad && t <= d; ++t) {
-        const T *z = (const T *)a.logits + ((int64_t)b * a.rows + t) * a.stride;
-        const Piece *pc = (const Piece *)a.stats + ((int64_t)b * a.rows + t) * pieces;
-        float top = -INFINITY;
-        int32_t arg = 0;
-        bool nan = false;
-        for (int32_t i = 0; i < pieces; ++i) {
-            nan |= !(pc[i].sum >= 0.0f);
-            if (pc[i].top > top) {
-                top = pc[i].top;
-                arg = pc[i].arg;
-            }
-        }
-        if (nan || top == -INFINITY || top == INFINITY) {
-            bad = true;
-            break;
-        }
-        double part = 0.0;
-        for (int32_t i = tid; i < v; i += kFinish)
-            part += exp(((double)to_f32(z[i]) - top) * inv);
-        const double total = block_sum(part, lds);
-        bool take = false;
-        const bool claimed = t < d && t < a.head &&
-                             !(a.src && t < 64 && ((a.src[b] >> t) & 1));
-        const float *q = claimed ? a.probs + ((int64_t)b * a.head + t) * v : nullptr;
-        if (t < d) {
-            const double p = exp(((double)to_f32(z[x[t]]) - top) * inv) / total;
-            take = greedy ? x[t] == arg : (double)u[t] * (q ? (double)q[x[t]] : 1.0) < p;
-        }
-        if (take) {
-            token = x[t];
-        } else if (greedy) {
-            token = arg;
+    const float c = kLog2e / (greedy ? 1.0f : tf);
+
+    float x[W * N];
+    float top = -INFINITY;
+    const int32_t lo = piece * kPiece + tid * N;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const int32_t i = lo + w * (kThreads * N);
+        if (i <= a.vocab - N) {
+            const Word<T> y = *(const Word<T> *)(z + i);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                x[w * N + k] = to_f32(y.x[k]);
         } else {
-            // weights of the draw: mode 0 the row's own, 1 without x_t, 2 the
-            // excess over q
-            int mode = t == d ? 0 : (q ? 2 : 1);
-            const auto weight = [&](int32_t i) {
-                const double w = exp(((double)to_f32(z[i]) - top) * inv);
-                if (mode == 1)
-                    return i == x[t] ? 0.0 : w;
-                const double e = w - (mode == 2 ? (double)q[i] * total : 0.0);
-                return e > 0.0 ? e : 0.0;
-            };
-            const int32_t per = (v + kFinish - 1) / kFinish;
-            const int32_t lo = tid * per < v ? tid * per : v;
-            const int32_t hi = lo + per < v ? lo + per : v;
-            double all = 0.0;
-            for (; mode >= 0; mode = mode == 2 ? 0 : -1) {
-                part = 0.0;
-                for (int32_t i = lo; i < hi; ++i)
-                    part += weight(i);
-                all = block_sum(part, lds);
-                if (all > 0.0 || mode == 0)
-                    break;
-            }
-            if (mode < 0)
-                mode = 0;
-            run[tid] = part;
-            if (tid == 0)
-                pick = last = -1;
-            __syncthreads();
-            double before = 0.0;
-            for (int w = 0; w < tid; ++w)
-                before += run[w];
-            const double goal = (double)u[a.rows - 1] * all;
-            for (int32_t i = lo; i < hi; ++i) {
-                const double w = weight(i);
-                if (w > 0.0) {
-                    if (before + w > goal) {
-                        if (before <= goal)
-                            atomicMax(&pick, i);
-                    }
-                    before += w;
-                    atomicMax(&last, i);
-                }
-            }
-            __syncthreads();
-            // the running sum's last rounding may end just at the goal
-            token = pick >= 0 ? pick : last;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                x[w * N + k] = i + k < a.vocab ? to_f32(z[i + k]) : -INFINITY;
         }
-        if (tid == 0) {
-            a.out_tokens[(int64_t)b * a.rows + t] = token;
-            if (a.out_logprobs)
-                a.out_logprobs[(int64_t)b * a.rows + t] =
-                    (float)(((double)to_f32(z[token]) - top) * inv - log(total));
+    }
+#pragma unroll
+    for (int k = 0; k < W * N; ++k)
+        top = fmaxf(top, x[k]);
+    top = wave_max(top);
+    if (lane == 0)
+        lds_max[wave] = top;
+    __syncthreads();
+    top = lds_max[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w)
+        top = fmaxf(top, lds_max[w]);
+    // (without a finite logit the sum is 0, or NaN with a NaN; what rounding
+    // took off the common exponent is put back into the sum)
+    const float base = top == -INFINITY ? 0.0f : top * c;
+    const float rest = top == -INFINITY ? 0.0f : fmaf(top, c, -base);
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W * N; ++k)
+        sum += __builtin_amdgcn_exp2f(fmaf(x[k], c, -base));
+    sum = wave_sum(sum);
+    int32_t arg = 0x7fffffff;
+    if (greedy) {
+#pragma unroll
+        for (int k = W * N - 1; k >= 0; --k)
+            if (x[k] == top)
+                arg = lo + k / N * (kThreads * N) + k % N;
+        for (int i = kWave / 2; i; i >>= 1) {
+            const int32_t y = __shfl_xor(arg, i);
+            arg = y < arg ? y : arg;
         }
-        accepted = t;
-        if (!take)
-            break;
     }
-    if (bad && tid == 0)
-        atomicOr(a.err, (uint32_t)kErrBlock);
-    const int32_t count = bad || d < 0 ? 0 : accepted + 1;
-    for (int32_t t = count + tid; t < a.rows; t += kFinish) {
-        a.out_tokens[(int64_t)b * a.rows + t] = -1;
-        if (a.out_logprobs)
-            a.out_logprobs[(int64_t)b * a.rows + t] = 0.0f;
+    if (lane == 0) {
+        lds_sum[wave] = sum;
+        lds_arg[wave] = arg;
     }
+    __syncthreads();
+    const int64_t r = (int64_t)b * a.rows + t;
     if (tid == 0) {
-        a.out_accepted[b] = count > 0 ? accepted : 0;
-        a.out_counts[b] = count;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) {
+            sum += lds_sum[w];
+            arg = lds_arg[w] < arg ? lds_arg[w] : arg;
+        }
+        sum *= __builtin_amdgcn_exp2f(-rest);
+        Piece *p = sp.pieces + r * pieces + piece;
+        poke(&p->top_sum, (unsigned long long)__float_as_uint(top) << 32 | __float_as_uint(sum));
+        if (greedy)
+            poke(&p->arg, (unsigned long long)(uint32_t)arg);
+        lds_say = arrive(sp.arrived + r) == (int32_t)pieces - 1;
+    }
+    __syncthreads();
+    if (!lds_say)
+        return;
+
+    // this workgroup completes the row: join the pieces and decide
+    __shared__ int32_t lds_verdict;
+    const double inv = greedy ? 1.0 : 1.0 / (double)tf;
+    const int32_t token = t < d ? a.draft[(int64_t)b * (a.rows - 1) + t] : -1;
+    const bool known = token >= 0 && token < a.vocab;
+    const float *q = claim_of(a, b, t, d);
+    const double weight = known && !greedy
+                              ? (double)a.uniform[r] * (q ? (double)q[token] : 1.0)
+                              : 0.0;
+    double total = 0.0, zx = 0.0;
+    if (wave == 0) {
+        float m = -INFINITY;
+        for (uint32_t i = lane; i < pieces; i += kWave)
+            m = fmaxf(m, __uint_as_float(
+                             (uint32_t)(peek(&sp.pieces[r * pieces + i].top_sum) >> 32)));
+        m = wave_max(m);
+        int32_t best = 0x7fffffff;
+        for (uint32_t i = lane; i < pieces; i += kWave) {
+            const unsigned long long v = peek(&sp.pieces[r * pieces + i].top_sum);
+            const float pt = __uint_as_float((uint32_t)(v >> 32));
+            const float ps = __uint_as_float((uint32_t)v);
+            total += pt == -INFINITY ? (double)ps : (double)ps * exp(((double)pt - m) * inv);
+            if (greedy && pt == m) {
+                const int32_t k = (int32_t)peek(&sp.pieces[r * pieces + i].arg);
+                best = k < best ? k : best;
+            }
+        }
+        total = wave_sum(total);
+        if (greedy)
+            for (int i = kWave / 2; i; i >>= 1) {
+                const int32_t y = __shfl_xor(best, i);
+                best = y < best ? y : best;
+            }
+        if (lane == 0) {
+            lds_top = m;
+            int32_t say = kRefuse;
+            bool close = false;
+            if (!(total > 0.0) || !(m < INFINITY)) {
+                say = kBad;
+            } else if (known) {
+                zx = ((double)to_f32(z[token]) - m) * inv;
+                const double p = exp(zx) / total;
+                say = (greedy ? token == best : weight < p) ? kAccept : kRefuse;
+                close = !greedy && fabs(weight - p) <= kClear * p;
+            }
+            lds_verdict = close ? -1 : say;
+            Row *row = sp.rows + r;
+            row->total = total;
+            row->top = m;
+            row->arg = best;
+            row->logp = known ? (float)(zx - log(total)) : 0.0f;
+            row->verdict = say;
+        }
+    }
+    __syncthreads();
+    if (lds_verdict < 0) {
+        const float m = lds_top;
+        double part = 0.0;
+        for (int32_t i = tid; i < a.vocab; i += kThreads)
+            part += exp(((double)to_f32(z[i]) - m) * inv);
+        part = block_sum(part, lds_d);
+        if (tid == 0) {
+            lds_verdict = weight < exp(zx) / part ? kAccept : kRefuse;
+            sp.rows[r].verdict = lds_verdict;
+        }
+    }
+    if (tid == 0 && lds_verdict != kAccept && t < d)
+        __hip_atomic_fetch_min(sp.stop + b, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What the rows decided, for one request; every thread of a workgroup gets it.
+struct Outcome {
+    int32_t d, at;    // at: the row that the last token comes from
+    bool none, bad;   // nothing to commit; because of a bad input
+};
+
+__device__ __forceinline__ Outcome outcome_of(const VerifyArgs &a, const Space &sp, int32_t b,
+                                              int32_t *lds)
+{
+    Outcome o;
+    o.d = a.draft_len[b];
+    o.at = 0;
+    const float tf = temperature(a, b);
+    o.bad = o.d < -1 || o.d >= a.rows || !(tf >= 0.0f) || tf == INFINITY;
+    o.none = o.bad || o.d < 0;
+    if (o.none)
+        return o;
+    const bool greedy = tf == 0.0f;
+    const int64_t r = (int64_t)b * a.rows;
+    if (threadIdx.x < kWave) {
+        int32_t at = o.d, bad = 0;
+        for (int32_t t = threadIdx.x; t <= o.d; t += kWave) {
+            const float u = a.uniform[t < o.d ? r + t : r + a.rows - 1];
+            if (!greedy && !(u >= 0.0f && u < 1.0f))
+                bad = 1;
+            if (t < o.d) {
+                const int32_t x = a.draft[(int64_t)b * (a.rows - 1) + t];
+                if (x < 0 || x >= a.vocab)
+                    bad = 1;
+                if (sp.rows[r + t].verdict != kAccept && t < at)
+                    at = t;
+            }
+        }
+        for (int i = kWave / 2; i; i >>= 1) {
+            const int32_t y = __shfl_xor(at, i);
+            at = y < at ? y : at;
+        }
+        bad = __any(bad) || sp.rows[r + at].verdict == kBad;
+        if (threadIdx.x == 0) {
+            lds[0] = at;
+            lds[1] = bad;
+        }
+    }
+    __syncthreads();
+    o.at = lds[0];
+    o.bad = lds[1] != 0;
+    o.none = o.bad;
+    return o;
+}
+
+// Writes a request's outputs and clears its counters; the whole workgroup.
+__device__ __forceinline__ void finish(const VerifyArgs &a, const Space &sp, int32_t b,
+                                       const Outcome &o, int32_t token, float logp)
+{
+    const int64_t r = (int64_t)b * a.rows;
+    for (int32_t t = threadIdx.x; t < a.rows; t += kThreads) {
+        const bool in = !o.none && t <= o.at, drafted = in && t < o.at;
+        a.out_tokens[r + t] = drafted ? a.draft[(int64_t)b * (a.rows - 1) + t] : (in ? token : -1);
+        if (a.out_logprobs)
+            a.out_logprobs[r + t] = drafted ? sp.rows[r + t].logp : (in ? logp : 0.0f);
+        sp.arrived[r + t] = 0;
+    }
+    if (threadIdx.x == 0) {
+        a.out_accepted[b] = o.none ? 0 : o.at;
+        a.out_counts[b] = o.none ? 0 : o.at + 1;
+        sp.stop[b] = kNever;
+        sp.drawn[b] = 0;
+        if (o.bad)
+            atomicOr(a.err, (uint32_t)kErrBlock);
     }
 }
 
-int32_t pieces_of(int32_t vocab) { return (vocab + kPiece - 1) / kPiece; }
+// Weight of token i of the row a request draws from: `out` is left out, and
+// with q only what exceeds it (scaled by the row's total) counts.
+template <typename T>
+__device__ __forceinline__ double weight_of(const T *z, int32_t i, double top, double inv,
+                                            int32_t out, const float *q, double total)
+{
+    const double w = i == out ? 0.0 : exp(((double)to_f32(z[i]) - top) * inv);
+    if (!q)
+        return w;
+    const double e = w - (double)q[i] * total;
+    return e > 0.0 ? e : 0.0;
+}
+
+// One workgroup per piece of a request's row to draw from. EXCESS 0: sums of
+// the weights; the last workgroup of a request without q at that row draws.
+// EXCESS 1 (a second launch, when there are drafter probabilities): sums of
+// the excess over q, whose total of the weights the first launch left.
+template <typename T, int EXCESS>
+__global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, int32_t draws)
+{
+    __shared__ double lds_d[kWaves];
+    __shared__ int32_t lds_o[2], lds_say, lds_piece, lds_pick, lds_last;
+    __shared__ double lds_before, lds_goal;
+    const int32_t b = blockIdx.x / (uint32_t)draws, piece = blockIdx.x % (uint32_t)draws;
+    const int32_t tid = threadIdx.x;
+    if (EXCESS) {
+        // requests that the first launch finished have cleared their row
+        // counters; those left have row 0's
+        if (sp.arrived[(int64_t)b * a.rows] == 0)
+            return;
+    }
+    const Outcome o = outcome_of(a, sp, b, lds_o);
+    const float tf = temperature(a, b);
+    const int64_t r = (int64_t)b * a.rows + o.at;
+    if (o.none || tf == 0.0f) {
+        if (piece == 0) {
+            __syncthreads();
+            const Row row = o.none ? Row{} : sp.rows[r];
+            const int32_t token = row.arg;
+            float logp = 0.0f;
+            if (!o.none)
+                logp = (float)-log(row.total);
+            finish(a, sp, b, o, token, logp);
+        }
+        return;
+    }
+    const Row row = sp.rows[r];
+    const T *z = (const T *)a.logits + r * a.stride;
+    const double inv = 1.0 / (double)tf, top = row.top;
+    const float *q = claim_of(a, b, o.at, o.d);
+    const int32_t out = o.at < o.d && !q ? a.draft[(int64_t)b * (a.rows - 1) + o.at] : -1;
+    double total = 0.0;
+    if (EXCESS) {
+        double part = 0.0;
+        for (int32_t i = tid; i < draws; i += kThreads)
+            part += sp.weights[(int64_t)b * draws + i];
+        total = block_sum(part, lds_d);
+    }
+    const float *over = EXCESS ? q : nullptr;
+    const int32_t lo = piece * kDraw;
+    double part = 0.0;
+#pragma unroll 4
+    for (int k = 0; k < kPer; ++k) {
+        const int32_t i = lo + k * kThreads + tid;
+        if (i < a.vocab)
+            part += weight_of(z, i, top, inv, out, over, total);
+    }
+    part = block_sum(part, lds_d);
+    double *sums = (EXCESS ? sp.excess : sp.weights) + (int64_t)b * draws;
+    if (tid == 0) {
+        poke(sums + piece, part);
+        lds_say = !EXCESS && q ? 0 : arrive(sp.drawn + b) == draws - 1;
+    }
+    __syncthreads();
+    if (!lds_say)
+        return;
+
+    // the last workgroup: the piece that holds the goal, then the token
+    if (tid < kWave) {
+        const double u = a.uniform[(int64_t)b * a.rows + a.rows - 1];
+        double all = 0.0;
+        for (int32_t i = tid; i < draws; i += kWave)
+            all += peek(sums + i);
+        all = wave_sum(all);
+        if (EXCESS && !(all > 0.0)) {  // (then it is 0)
+            // nothing exceeds q: draw from the weights
+            over = nullptr;
+            sums = sp.weights + (int64_t)b * draws;
+            for (int32_t i = tid; i < draws; i += kWave)
+                all += peek(sums + i);
+            all = wave_sum(all);
+        }
+        const double goal = u * all;
+        double before = 0.0, at_before = 0.0;
+        int32_t at = -1;
+        for (int32_t base = 0; base < draws; base += kWave) {
+            const double s = base + tid < draws ? peek(sums + base + tid) : 0.0;
+            double run = s;  // inclusive
+            for (int i = 1; i < kWave; i <<= 1) {
+                const double y = __shfl_up(run, i);
+                if (tid >= i)
+                    run += y;
+            }
+            const unsigned long long over_goal = __ballot(s > 0.0 && before + run > goal);
+            const unsigned long long live = __ballot(s > 0.0);
+            if (live) {
+                // (the last piece with a weight stands in if rounding left none)
+                const int k = over_goal ? __builtin_ctzll(over_goal) : 63 - __builtin_clzll(live);
+                at = base + k;
+                at_before = before + __shfl(run, k) - __shfl(s, k);
+            }
+            before += __shfl(run, kWave - 1);
+            if (over_goal)
+                break;
+        }
+        if (tid == 0) {
+            lds_piece = at;
+            lds_before = at_before;
+            lds_goal = goal;
+            lds_pick = 0x7fffffff;
+            lds_last = -1;
+            lds_say = over != nullptr;
+        }
+    }
+    __syncthreads();
+    over = lds_say ? q : nullptr;
+    const int32_t from = lds_piece * kDraw + tid * kPer;
+    double w[kPer], run = 0.0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        w[k] = lds_piece >= 0 && from + k < a.vocab
+                   ? weight_of(z, from + k, top, inv, out, over, total)
+                   : 0.0;
+        run += w[k];
+    }
+    // exclusive running sum over the threads
+    double incl = run;
+    const int lane = tid % kWave, wave = tid / kWave;
+    for (int i = 1; i < kWave; i <<= 1) {
+        const double y = __shfl_up(incl, i);
+        if (lane >= i)
+            incl += y;
+    }
+    if (lane == kWave - 1)
+        lds_d[wave] = incl;
+    __syncthreads();
+    double before = lds_before + incl - run;
+    for (int i = 0; i < wave; ++i)
+        before += lds_d[i];
+    int32_t pick = 0x7fffffff, last = -1;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+        if (w[k] > 0.0) {
+            before += w[k];
+            last = from + k;
+            if (before > lds_goal && pick == 0x7fffffff)
+                pick = from + k;
+        }
+    atomicMin(&lds_pick, pick);
+    atomicMax(&lds_last, last);
+    __syncthreads();
+    int32_t token = lds_pick != 0x7fffffff ? lds_pick : lds_last;
+    if (token < 0)
+        token = out >= 0 ? out : 0;  // no weight at all: the left-out token had it all
+    finish(a, sp, b, o, token,
+           (float)(((double)to_f32(z[token]) - top) * inv - log(row.total)));
+}
+
+template <typename K>
+hipError_t start(K kernel, const VerifyArgs &a, const Space &sp, int64_t groups, int64_t pieces,
+                 hipStream_t s)
+{
+    if (groups * pieces > 0x7fffffffLL)
+        return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(groups * pieces)), dim3(kThreads), 0, s, a, sp,
+                       pieces);
+    return hipGetLastError();
+}
 
 template <typename T>
 hipError_t launch_typed(const VerifyArgs &a, hipStream_t s)
 {
-    const int32_t pieces = pieces_of(a.vocab);
-    hipLaunchKernelGGL((stats_kernel<T>), dim3(pieces, a.rows, a.batch), dim3(kWave), 0, s, a);
-    hipLaunchKernelGGL((finish_kernel<T>), dim3(a.batch), dim3(kFinish), 0, s, a, pieces);
-    return hipGetLastError();
+    const Space sp = space_of((char *)a.stats, a.max_batch, a.max_rows, a.vocab, nullptr);
+    // 8,192 logits a piece, or 2,048 while that leaves the chip half empty
+    constexpr int kWide = 8192 / (16 / sizeof(T)) / kThreads;
+    const int64_t rows = (int64_t)a.batch * a.rows;
+    hipError_t e = pieces_of(a.vocab, 8192) * rows >= 512
+                       ? start(stats_kernel<T, kWide>, a, sp, rows, pieces_of(a.vocab, 8192), s)
+                       : start(stats_kernel<T, kWide / 4>, a, sp, rows,
+                               pieces_of(a.vocab, kMinPiece), s);
+    if (e == hipSuccess)
+        e = start(draw_kernel<T, 0>, a, sp, a.batch, pieces_of(a.vocab, kDraw), s);
+    if (e == hipSuccess && a.head > 0)
+        e = start(draw_kernel<T, 1>, a, sp, a.batch, pieces_of(a.vocab, kDraw), s);
+    return e;
 }
 
 }  // namespace
 
 size_t verify_workspace(int32_t batch, int32_t rows, int32_t vocab)
 {
-    return (size_t)batch * rows * pieces_of(vocab) * sizeof(Piece);
+    size_t size;
+    (void)space_of(nullptr, batch, rows, vocab, &size);
+    return size;
+}
+
+hipError_t verify_clear(void *ws, int32_t batch, int32_t rows, int32_t vocab, hipStream_t s)
+{
+    const Space sp = space_of((char *)ws, batch, rows, vocab, nullptr);
+    hipError_t e = hipMemsetAsync(sp.arrived, 0, (char *)sp.stop - (char *)sp.arrived, s);
+    if (e == hipSuccess)
+        e = hipMemsetAsync(sp.stop, kNever & 0xff, batch * sizeof(int32_t), s);
+    return e;
 }
 
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t s)
