@@ -1,4 +1,15 @@
 // Rotary positions and the paged cache's writer, for gfx950 (MI355X).
+//
+// Mathematics: a pair (x, y) at position p becomes g (x cos a - y sin a,
+// x sin a + y cos a), a = p f. The angle is kept in turns, as a 64-bit product
+// whose whole part is dropped (at position 262,144 a 32-bit product would be
+// off by 2^-6 radians); sine and cosine of the rest are 32-bit.
+//
+// Bound by memory: every element is read and written once. A row's angles
+// are the same for all its heads, so a workgroup computes them once into LDS
+// and then streams the heads in 16-byte words. V pages hold positions side by
+// side: a workgroup collects 64 positions of a head in LDS and stores them
+// along the positions, 16 bytes at a time where 8 positions are its own.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -9,18 +20,208 @@ namespace pld {
 
 namespace {
 
-// cos and sin of the angle `turns` per position reaches at position p: the
-// angle is reduced to one turn in 64 bits (at position 262,144 a 32-bit
-// product would be off by 2^-6 radians), the functions are 32-bit.
-__device__ __forceinline__ void turn(double turns, int32_t p, float &c, float &s)
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 128;   // head_dim 256
+constexpr int kSpan = 64;        // positions of a V tile
+constexpr int kPad = 2;          // elements between rows of the V tile
+
+typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void turn(double turns, int32_t p, float gain, float &c, float &s)
 {
     const double x = turns * p;
     sincospif((float)(2.0 * (x - rint(x))), &s, &c);
+    c *= gain;
+    s *= gain;
 }
 
-// One workgroup per row of a block.
+// 8 elements of T.
+template <typename T>
+struct Eight {
+    T x[8];
+};
+
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const T *p)
+{
+    return __builtin_bit_cast(Eight<T>, *(const U4 *)p);
+}
+
+// Stores 8 values rounded to C: 16 or 8 bytes.
+template <typename C>
+__device__ __forceinline__ void store8(C *p, const float (&y)[8])
+{
+    Eight<C> w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w.x[i] = from_f32<C>(y[i]);
+    struct __attribute__((aligned(8 * sizeof(C)))) Out {
+        Eight<C> w;
+    };
+    *(Out *)p = Out{w};
+}
+
+// Words of 8 elements: q, k and v 16-byte aligned with strides of 8 elements,
+// and rotated pairs that fill whole words.
+//
+// The first `turning` workgroups rotate R rows each, the others store V: one
+// per request, kv head and tile of kSpan positions.
+template <typename T, typename C, int R>
+__global__ __launch_bounds__(kThreads) void append_words(KvAppendArgs a, uint32_t turning,
+                                                         uint32_t tiles)
+{
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    const BlockArgs &g = a.blk;
+    const int32_t dim = g.head_dim, tokens = 1 << g.page_shift, tid = threadIdx.x;
+    int32_t length;
+    uint32_t err;
+    if (blockIdx.x >= turning) {
+        const uint32_t id = blockIdx.x - turning;
+        const int32_t h = id % (uint32_t)g.kv_heads;
+        const uint32_t bt = id / (uint32_t)g.kv_heads;
+        const int32_t b = bt / tiles;
+        const int32_t n = block_rows(g, b, length, err);
+        if (n <= 0)
+            return;
+        // the tile's positions, and those of them the block has
+        const int64_t p0 = ((int64_t)(length - 1) / kSpan + bt % tiles) * kSpan;
+        const int64_t from = p0 > length - 1 ? p0 : length - 1;
+        const int64_t last = (int64_t)length - 1 + n;
+        const int64_t to = p0 + kSpan < last ? p0 + kSpan : last;
+        if (from >= to)
+            return;
+        T *tile = (T *)lds;
+        const int32_t pitch = dim + kPad, words = dim / 8;
+        const T *v = (const T *)a.v + ((int64_t)b * g.rows - (length - 1)) * a.kv_stride +
+                     (int64_t)h * dim;
+        for (int32_t i = tid; i < (int32_t)(to - from) * words; i += kThreads) {
+            const int64_t p = from + i / words;
+            const int32_t d = i % words * 8;
+            const Eight<T> x = load8(v + p * a.kv_stride + d);
+            T *row = tile + (int32_t)(p - p0) * pitch + d;
+            // (rows are padded: 4 bytes at a time)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                ((uint32_t *)row)[k] = __builtin_bit_cast(U4, x)[k];
+        }
+        __syncthreads();
+        const float scale = g.v_scale ? g.v_scale[h] : 1.0f;
+        for (int32_t i = tid; i < kSpan / 8 * dim; i += kThreads) {
+            const int32_t d = i / (kSpan / 8), at = i % (kSpan / 8) * 8;
+            const int64_t p = p0 + at;
+            if (p + 8 <= from || p >= to)
+                continue;
+            const int32_t page = page_of(g, b, (int32_t)(p > from ? p : from));
+            if (page < 0)
+                continue;  // (reported by the row's K)
+            C *out = (C *)a.v_cache + (((int64_t)page * g.kv_heads + h) * dim + d) * tokens +
+                     (p & (tokens - 1));
+            const bool whole = p >= from && p + 8 <= to;
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                y[k] = whole || (p + k >= from && p + k < to)
+                           ? to_f32(tile[(at + k) * pitch + d]) / scale
+                           : 0.0f;
+            if (whole) {
+                store8<C>(out, y);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (p + k >= from && p + k < to)
+                        out[k] = from_f32<C>(y[k]);
+            }
+        }
+        return;
+    }
+
+    // rotate q and k of R rows
+    float2 *cs = (float2 *)lds;
+    const int32_t pairs = a.rot_dim / 2;
+    const uint32_t groups = (uint32_t)(g.rows + R - 1) / R;
+    const int32_t b = blockIdx.x / groups, t0 = blockIdx.x % groups * R;
+    const int32_t n = block_rows(g, b, length, err);
+    if (t0 >= n) {
+        if (err && t0 == 0 && tid == 0)
+            atomicOr(g.err, err);
+        return;
+    }
+    const int32_t live = n - t0 < R ? n - t0 : R;
+    for (int32_t i = tid; i < live * pairs; i += kThreads) {
+        float c, s;
+        turn(a.turns[i % pairs], length - 1 + t0 + i / pairs, a.magnitude, c, s);
+        cs[i] = float2{c, s};
+    }
+    __syncthreads();
+    // units of a head: with the half layout a word of the first half and its
+    // partner are one, else every word is one
+    const int32_t twos = a.interleaved ? 0 : pairs / 8;
+    const int32_t units = dim / 8 - twos;
+    const int32_t q_heads = a.q ? g.q_heads : 0, heads = q_heads + g.kv_heads;
+    for (int32_t i = tid; i < live * heads * units; i += kThreads) {
+        const int32_t unit = i % units, hr = i / units, h = hr % heads, t = hr / heads;
+        const int32_t p = length - 1 + t0 + t;
+        const int64_t r = (int64_t)b * g.rows + t0 + t;
+        const bool is_q = h < q_heads;
+        const T *x = is_q ? (const T *)a.q + r * a.q_stride + (int64_t)h * dim
+                          : (const T *)a.k + r * a.kv_stride + (int64_t)(h - q_heads) * dim;
+        const float2 *w = cs + t * pairs;
+        const int32_t d = unit < twos ? unit * 8 : (unit + twos) * 8;
+        float y[8], z[8];
+        const Eight<T> u = load8(x + d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            y[k] = to_f32(u.x[k]);
+        if (unit < twos) {
+            const Eight<T> v = load8(x + d + pairs);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float e = y[k], f = to_f32(v.x[k]);
+                const float2 m = w[d + k];
+                y[k] = e * m.x - f * m.y;
+                z[k] = e * m.y + f * m.x;
+            }
+        } else if (d < a.rot_dim) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                const float e = y[k], f = y[k + 1];
+                const float2 m = w[(d + k) / 2];
+                y[k] = e * m.x - f * m.y;
+                y[k + 1] = e * m.y + f * m.x;
+            }
+        }
+        if (is_q) {
+            T *out = (T *)a.out_q + (r * g.q_heads + h) * dim + d;
+            store8<T>(out, y);
+            if (unit < twos)
+                store8<T>(out + pairs, z);
+            continue;
+        }
+        const int32_t page = page_of(g, b, p);
+        if (page < 0) {
+            atomicOr(g.err, (uint32_t)kErrPage);
+            continue;
+        }
+        if (g.k_scale) {
+            const float scale = g.k_scale[h - q_heads];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                y[k] /= scale;
+                z[k] /= scale;
+            }
+        }
+        C *out = (C *)a.k_cache +
+                 (((int64_t)page * g.kv_heads + h - q_heads) * tokens + (p & (tokens - 1))) * dim + d;
+        store8<C>(out, y);
+        if (unit < twos)
+            store8<C>(out + pairs, z);
+    }
+}
+
+// Any alignment and any part of a head: one workgroup per row, an element at
+// a time.
 template <typename T, typename C>
-__global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a)
+__global__ __launch_bounds__(kThreads) void append_elements(KvAppendArgs a)
 {
     const BlockArgs &g = a.blk;
     const int32_t t = (int32_t)(blockIdx.x % (uint32_t)g.rows);
@@ -41,27 +242,35 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a)
     const int32_t slot = p & (tokens - 1);
     const int64_t r = (int64_t)b * g.rows + t;
     const int32_t heads = a.q ? g.q_heads : 0;
-    for (int32_t i = threadIdx.x; i < (heads + g.kv_heads) * dim; i += blockDim.x) {
-        const int32_t h = i / dim, d = i % dim;
-        const bool is_q = h < heads;
+    // (both elements of a pair go through one thread: q may be rotated in place)
+    const int32_t units = dim - half;
+    for (int32_t i = threadIdx.x; i < (heads + g.kv_heads) * units; i += blockDim.x) {
+        const int32_t h = i / units, e = i % units;
+        const bool is_q = h < heads, two = e < half;
         const T *x = is_q ? (const T *)a.q + r * a.q_stride + (int64_t)h * dim
                           : (const T *)a.k + r * a.kv_stride + (int64_t)(h - heads) * dim;
-        float y = to_f32(x[d]);
-        if (d < a.rot_dim) {
-            const int32_t i2 = a.interleaved ? d / 2 : (d < half ? d : d - half);
-            const bool first = a.interleaved ? !(d & 1) : d < half;
-            const int32_t other = a.interleaved ? (d ^ 1) : (first ? d + half : d - half);
+        const int32_t d = two ? (a.interleaved ? 2 * e : e) : e + half;
+        const int32_t d2 = two ? (a.interleaved ? d + 1 : d + half) : d;
+        float y = to_f32(x[d]), z = to_f32(x[d2]);
+        if (two) {
             float c, s;
-            turn(a.turns[i2], p, c, s);
-            const float z = to_f32(x[other]);
-            y = (first ? y * c - z * s : z * s + y * c) * a.magnitude;
+            turn(a.turns[e], p, a.magnitude, c, s);
+            const float y0 = y;
+            y = y0 * c - z * s;
+            z = y0 * s + z * c;
         }
         if (is_q) {
-            ((T *)a.out_q)[r * g.q_heads * dim + (int64_t)h * dim + d] = from_f32<T>(y);
+            T *out = (T *)a.out_q + (r * g.q_heads + h) * dim;
+            out[d] = from_f32<T>(y);
+            if (two)
+                out[d2] = from_f32<T>(z);
         } else if (page >= 0) {
             const float scale = g.k_scale ? g.k_scale[h - heads] : 1.0f;
-            ((C *)a.k_cache)[(((int64_t)page * g.kv_heads + h - heads) * tokens + slot) * dim + d] =
-                from_f32<C>(y / scale);
+            C *out = (C *)a.k_cache +
+                     (((int64_t)page * g.kv_heads + h - heads) * tokens + slot) * dim;
+            out[d] = from_f32<C>(y / scale);
+            if (two)
+                out[d2] = from_f32<C>(z / scale);
         }
     }
     if (page < 0)
@@ -73,25 +282,47 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a)
     }
 }
 
-template <typename T>
-void launch_typed(const KvAppendArgs &a, hipStream_t s)
+template <typename T, typename C>
+hipError_t launch_cells(const KvAppendArgs &a, hipStream_t s)
 {
-    const dim3 grid((uint32_t)a.blk.batch * (uint32_t)a.blk.rows);
-    if (a.blk.cache_dtype == PLD_E4M3)
-        hipLaunchKernelGGL((kv_append_kernel<T, E4m3>), grid, dim3(256), 0, s, a);
+    const BlockArgs &g = a.blk;
+    const int64_t rows = (int64_t)g.batch * g.rows;
+    const bool words = !(((uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.out_q) &
+                         15u) &&
+                       !((a.q ? a.q_stride : 0) & 7) && !(a.kv_stride & 7) &&
+                       a.rot_dim % (a.interleaved ? 8 : 16) == 0;
+    if (!words) {
+        hipLaunchKernelGGL((append_elements<T, C>), dim3((uint32_t)rows), dim3(kThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    // 4 rows a workgroup share its start once there are enough of them
+    const int R = rows > 2048 ? 4 : 1;
+    const int64_t turning = (int64_t)g.batch * ((g.rows + R - 1) / R);
+    const int64_t tiles = (g.rows + kSpan - 2) / kSpan + 1;
+    const int64_t storing = (int64_t)g.batch * g.kv_heads * tiles;
+    if (turning + storing > 0x7fffffffLL)
+        return hipErrorInvalidConfiguration;
+    const size_t turn_lds = (size_t)R * kMaxPairs * sizeof(float2);
+    const size_t tile_lds = (size_t)kSpan * (g.head_dim + kPad) * sizeof(T);
+    const size_t lds = turn_lds > tile_lds ? turn_lds : tile_lds;
+    const dim3 grid((uint32_t)(turning + storing));
+    if (R == 4)
+        hipLaunchKernelGGL((append_words<T, C, 4>), grid, dim3(kThreads), lds, s, a,
+                           (uint32_t)turning, (uint32_t)tiles);
     else
-        hipLaunchKernelGGL((kv_append_kernel<T, T>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((append_words<T, C, 1>), grid, dim3(kThreads), lds, s, a,
+                           (uint32_t)turning, (uint32_t)tiles);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s)
 {
+    const bool wide = a.blk.cache_dtype != PLD_E4M3;
     if (a.blk.dtype == PLD_BF16)
-        launch_typed<__bf16>(a, s);
-    else
-        launch_typed<_Float16>(a, s);
-    return hipGetLastError();
+        return wide ? launch_cells<__bf16, __bf16>(a, s) : launch_cells<__bf16, E4m3>(a, s);
+    return wide ? launch_cells<_Float16, _Float16>(a, s) : launch_cells<_Float16, E4m3>(a, s);
 }
 
 }  // namespace pld

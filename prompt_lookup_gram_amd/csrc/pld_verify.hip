@@ -38,7 +38,9 @@ constexpr int kWave = 64;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kDraw = 4096;                 // logits of a draw's piece
-constexpr int kPer = kDraw / kThreads;      // of a thread
+constexpr int kDrawThreads = 512;
+constexpr int kDrawWaves = kDrawThreads / kWave;
+constexpr int kPer = kDraw / kDrawThreads;  // of a thread
 constexpr int32_t kNever = 0x7f7f7f7f;      // `stop` before a refusal
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kClear = 1.0 / 65536;      // relative distance that 32 bits decide
@@ -150,7 +152,7 @@ __device__ __forceinline__ double block_sum(double x, double *lds)
         lds[threadIdx.x / kWave] = x;
     __syncthreads();
     double s = 0.0;
-    for (int w = 0; w < kWaves; ++w)
+    for (int w = 0; w < (int)blockDim.x / kWave; ++w)
         s += lds[w];
     return s;
 }
@@ -178,9 +180,6 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a, Space sp,
     constexpr int kPiece = W * N * kThreads;
     __shared__ float lds_max[kWaves], lds_sum[kWaves];
     __shared__ int32_t lds_arg[kWaves];
-    __shared__ int32_t lds_say;
-    __shared__ float lds_top;
-    __shared__ double lds_d[kWaves];
     const int32_t piece = blockIdx.x % pieces, tid = threadIdx.x;
     const uint32_t order = blockIdx.x / pieces;
     const int32_t b = order % (uint32_t)a.batch, t = order / (uint32_t)a.batch;
@@ -192,6 +191,14 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a, Space sp,
     const float tf = temperature(a, b);
     const bool greedy = tf == 0.0f;
     const float c = kLog2e / (greedy ? 1.0f : tf);
+
+    // what deciding the row takes, on its way with the row
+    const int32_t token = t < d ? a.draft[(int64_t)b * (a.rows - 1) + t] : -1;
+    const bool known = token >= 0 && token < a.vocab;
+    const float *q = claim_of(a, b, t, d);
+    const float claim = q && known ? q[token] : 1.0f;
+    const float z_token = known ? to_f32(z[token]) : 0.0f;
+    const float u = a.uniform[(int64_t)b * a.rows + t];
 
     float x[W * N];
     float top = -INFINITY;
@@ -246,141 +253,124 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a, Space sp,
         lds_arg[wave] = arg;
     }
     __syncthreads();
+    if (wave > 0)
+        return;  // one wavefront counts the piece in, and decides if it is the last
     const int64_t r = (int64_t)b * a.rows + t;
-    if (tid == 0) {
+    Piece *const mine = sp.pieces + r * pieces;
+    int32_t count = 0;
+    if (lane == 0) {
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) {
             sum += lds_sum[w];
             arg = lds_arg[w] < arg ? lds_arg[w] : arg;
         }
         sum *= __builtin_amdgcn_exp2f(-rest);
-        Piece *p = sp.pieces + r * pieces + piece;
-        poke(&p->top_sum, (unsigned long long)__float_as_uint(top) << 32 | __float_as_uint(sum));
+        poke(&mine[piece].top_sum,
+             (unsigned long long)__float_as_uint(top) << 32 | __float_as_uint(sum));
         if (greedy)
-            poke(&p->arg, (unsigned long long)(uint32_t)arg);
-        lds_say = arrive(sp.arrived + r) == (int32_t)pieces - 1;
+            poke(&mine[piece].arg, (unsigned long long)(uint32_t)arg);
+        count = arrive(sp.arrived + r);
     }
-    __syncthreads();
-    if (!lds_say)
+    if (__builtin_amdgcn_readfirstlane(count) != (int32_t)pieces - 1)
         return;
 
-    // this workgroup completes the row: join the pieces and decide
-    __shared__ int32_t lds_verdict;
+    // this wavefront completes the row: join the pieces and decide
     const double inv = greedy ? 1.0 : 1.0 / (double)tf;
-    const int32_t token = t < d ? a.draft[(int64_t)b * (a.rows - 1) + t] : -1;
-    const bool known = token >= 0 && token < a.vocab;
-    const float *q = claim_of(a, b, t, d);
-    const double weight = known && !greedy
-                              ? (double)a.uniform[r] * (q ? (double)q[token] : 1.0)
-                              : 0.0;
-    double total = 0.0, zx = 0.0;
-    if (wave == 0) {
-        float m = -INFINITY;
-        for (uint32_t i = lane; i < pieces; i += kWave)
-            m = fmaxf(m, __uint_as_float(
-                             (uint32_t)(peek(&sp.pieces[r * pieces + i].top_sum) >> 32)));
-        m = wave_max(m);
-        int32_t best = 0x7fffffff;
-        for (uint32_t i = lane; i < pieces; i += kWave) {
-            const unsigned long long v = peek(&sp.pieces[r * pieces + i].top_sum);
-            const float pt = __uint_as_float((uint32_t)(v >> 32));
-            const float ps = __uint_as_float((uint32_t)v);
-            total += pt == -INFINITY ? (double)ps : (double)ps * exp(((double)pt - m) * inv);
-            if (greedy && pt == m) {
-                const int32_t k = (int32_t)peek(&sp.pieces[r * pieces + i].arg);
-                best = k < best ? k : best;
-            }
-        }
-        total = wave_sum(total);
-        if (greedy)
-            for (int i = kWave / 2; i; i >>= 1) {
-                const int32_t y = __shfl_xor(best, i);
-                best = y < best ? y : best;
-            }
-        if (lane == 0) {
-            lds_top = m;
-            int32_t say = kRefuse;
-            bool close = false;
-            if (!(total > 0.0) || !(m < INFINITY)) {
-                say = kBad;
-            } else if (known) {
-                zx = ((double)to_f32(z[token]) - m) * inv;
-                const double p = exp(zx) / total;
-                say = (greedy ? token == best : weight < p) ? kAccept : kRefuse;
-                close = !greedy && fabs(weight - p) <= kClear * p;
-            }
-            lds_verdict = close ? -1 : say;
-            Row *row = sp.rows + r;
-            row->total = total;
-            row->top = m;
-            row->arg = best;
-            row->logp = known ? (float)(zx - log(total)) : 0.0f;
-            row->verdict = say;
+    const double weight = greedy ? 0.0 : (double)u * (double)claim;
+    float m = -INFINITY;
+    for (uint32_t i = lane; i < pieces; i += kWave)
+        m = fmaxf(m, __uint_as_float((uint32_t)(peek(&mine[i].top_sum) >> 32)));
+    m = wave_max(m);
+    int32_t best = 0x7fffffff;
+    double total = 0.0;
+    for (uint32_t i = lane; i < pieces; i += kWave) {
+        const unsigned long long v = peek(&mine[i].top_sum);
+        const float pt = __uint_as_float((uint32_t)(v >> 32));
+        const float ps = __uint_as_float((uint32_t)v);
+        total += pt == -INFINITY ? (double)ps : (double)ps * exp(((double)pt - m) * inv);
+        if (greedy && pt == m) {
+            const int32_t k = (int32_t)peek(&mine[i].arg);
+            best = k < best ? k : best;
         }
     }
-    __syncthreads();
-    if (lds_verdict < 0) {
-        const float m = lds_top;
-        double part = 0.0;
-        for (int32_t i = tid; i < a.vocab; i += kThreads)
-            part += exp(((double)to_f32(z[i]) - m) * inv);
-        part = block_sum(part, lds_d);
-        if (tid == 0) {
-            lds_verdict = weight < exp(zx) / part ? kAccept : kRefuse;
-            sp.rows[r].verdict = lds_verdict;
+    total = wave_sum(total);
+    if (greedy)
+        for (int i = kWave / 2; i; i >>= 1) {
+            const int32_t y = __shfl_xor(best, i);
+            best = y < best ? y : best;
+        }
+    int32_t say = kRefuse;
+    float logp = 0.0f;
+    if (!(total > 0.0) || !(m < INFINITY)) {
+        say = kBad;
+    } else if (known) {
+        const double zx = ((double)z_token - m) * inv, p = exp(zx) / total;
+        logp = (float)(zx - log(total));
+        if (!greedy && fabs(weight - p) <= kClear * p) {
+            double sure = 0.0;
+            for (int32_t i = lane; i < a.vocab; i += kWave)
+                sure += exp(((double)to_f32(z[i]) - m) * inv);
+            say = weight < exp(zx) / wave_sum(sure) ? kAccept : kRefuse;
+        } else {
+            say = (greedy ? token == best : weight < p) ? kAccept : kRefuse;
         }
     }
-    if (tid == 0 && lds_verdict != kAccept && t < d)
-        __hip_atomic_fetch_min(sp.stop + b, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (lane == 0) {
+        sp.rows[r] = Row{total, m, logp, best, say, {0, 0}};
+        if (say != kAccept && t < d)
+            __hip_atomic_fetch_min(sp.stop + b, t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
 }
 
-// What the rows decided, for one request; every thread of a workgroup gets it.
+// What the rows decided, for one request.
 struct Outcome {
     int32_t d, at;    // at: the row that the last token comes from
+    int32_t out;      // that row's draft token (-1: none)
+    float u;          // the draw's random number
+    Row row;          // the row
     bool none, bad;   // nothing to commit; because of a bad input
 };
 
-__device__ __forceinline__ Outcome outcome_of(const VerifyArgs &a, const Space &sp, int32_t b,
-                                              int32_t *lds)
+// The same on every wavefront: each reads what it takes. Lane t looks at row
+// t (then at row t + 64, ...), all its loads issued at once; what rows past
+// the last token hold (some other call's verdicts) is not used.
+__device__ __forceinline__ Outcome outcome_of(const VerifyArgs &a, const Space &sp, int32_t b)
 {
     Outcome o;
-    o.d = a.draft_len[b];
-    o.at = 0;
-    const float tf = temperature(a, b);
-    o.bad = o.d < -1 || o.d >= a.rows || !(tf >= 0.0f) || tf == INFINITY;
-    o.none = o.bad || o.d < 0;
-    if (o.none)
-        return o;
-    const bool greedy = tf == 0.0f;
     const int64_t r = (int64_t)b * a.rows;
-    if (threadIdx.x < kWave) {
-        int32_t at = o.d, bad = 0;
-        for (int32_t t = threadIdx.x; t <= o.d; t += kWave) {
-            const float u = a.uniform[t < o.d ? r + t : r + a.rows - 1];
-            if (!greedy && !(u >= 0.0f && u < 1.0f))
-                bad = 1;
-            if (t < o.d) {
-                const int32_t x = a.draft[(int64_t)b * (a.rows - 1) + t];
-                if (x < 0 || x >= a.vocab)
-                    bad = 1;
-                if (sp.rows[r + t].verdict != kAccept && t < at)
-                    at = t;
-            }
-        }
-        for (int i = kWave / 2; i; i >>= 1) {
-            const int32_t y = __shfl_xor(at, i);
-            at = y < at ? y : at;
-        }
-        bad = __any(bad) || sp.rows[r + at].verdict == kBad;
-        if (threadIdx.x == 0) {
-            lds[0] = at;
-            lds[1] = bad;
+    const int lane = threadIdx.x % kWave;
+    o.d = a.draft_len[b];
+    o.u = a.uniform[r + a.rows - 1];
+    const float tf = temperature(a, b);
+    const bool greedy = tf == 0.0f;
+    bool bad = !(tf >= 0.0f) || tf == INFINITY || o.d < -1 || o.d >= a.rows;
+    o.at = o.d;
+    o.out = -1;
+    o.row = Row{};
+    bool found = false;
+    for (int32_t base = 0; base < a.rows; base += kWave) {
+        const int32_t t = base + lane, in = t < a.rows ? t : a.rows - 1;
+        const Row row = sp.rows[r + in];
+        const float u = a.uniform[r + in];
+        const int32_t x = in < a.rows - 1 ? a.draft[(int64_t)b * (a.rows - 1) + in] : -1;
+        if (t < o.d && (x < 0 || x >= a.vocab || (!greedy && !(u >= 0.0f && u < 1.0f))))
+            bad = true;
+        const uint64_t ends = __ballot(t == o.d || (t < o.d && row.verdict != kAccept));
+        if (ends && !found) {
+            found = true;
+            const int k = __builtin_ctzll(ends);
+            o.at = base + k;
+            o.out = o.at < o.d ? __shfl(x, k) : -1;
+            o.row.total = __shfl(row.total, k);
+            o.row.top = __shfl(row.top, k);
+            o.row.arg = __shfl(row.arg, k);
+            o.row.verdict = __shfl(row.verdict, k);
         }
     }
-    __syncthreads();
-    o.at = lds[0];
-    o.bad = lds[1] != 0;
-    o.none = o.bad;
+    if (!greedy && o.d >= 0 && !(o.u >= 0.0f && o.u < 1.0f))
+        bad = true;
+    o.bad = __any(bad) || (o.d >= 0 && o.row.verdict == kBad);
+    o.none = o.bad || o.d < 0;
     return o;
 }
 
@@ -389,7 +379,7 @@ __device__ __forceinline__ void finish(const VerifyArgs &a, const Space &sp, int
                                        const Outcome &o, int32_t token, float logp)
 {
     const int64_t r = (int64_t)b * a.rows;
-    for (int32_t t = threadIdx.x; t < a.rows; t += kThreads) {
+    for (int32_t t = threadIdx.x; t < a.rows; t += kDrawThreads) {
         const bool in = !o.none && t <= o.at, drafted = in && t < o.at;
         a.out_tokens[r + t] = drafted ? a.draft[(int64_t)b * (a.rows - 1) + t] : (in ? token : -1);
         if (a.out_logprobs)
@@ -424,10 +414,11 @@ __device__ __forceinline__ double weight_of(const T *z, int32_t i, double top, d
 // EXCESS 1 (a second launch, when there are drafter probabilities): sums of
 // the excess over q, whose total of the weights the first launch left.
 template <typename T, int EXCESS>
-__global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, int32_t draws)
+__global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space sp, int32_t draws)
 {
-    __shared__ double lds_d[kWaves];
-    __shared__ int32_t lds_o[2], lds_say, lds_piece, lds_pick, lds_last;
+    __shared__ double lds_d[kDrawWaves];
+    __shared__ int32_t lds_say, lds_piece, lds_pick, lds_last;
+    __shared__ float lds_z;
     __shared__ double lds_before, lds_goal;
     const int32_t b = blockIdx.x / (uint32_t)draws, piece = blockIdx.x % (uint32_t)draws;
     const int32_t tid = threadIdx.x;
@@ -437,39 +428,30 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
         if (sp.arrived[(int64_t)b * a.rows] == 0)
             return;
     }
-    const Outcome o = outcome_of(a, sp, b, lds_o);
+    const Outcome o = outcome_of(a, sp, b);
     const float tf = temperature(a, b);
-    const int64_t r = (int64_t)b * a.rows + o.at;
     if (o.none || tf == 0.0f) {
-        if (piece == 0) {
-            __syncthreads();
-            const Row row = o.none ? Row{} : sp.rows[r];
-            const int32_t token = row.arg;
-            float logp = 0.0f;
-            if (!o.none)
-                logp = (float)-log(row.total);
-            finish(a, sp, b, o, token, logp);
-        }
+        if (piece == 0)
+            finish(a, sp, b, o, o.row.arg, o.none ? 0.0f : (float)-log(o.row.total));
         return;
     }
-    const Row row = sp.rows[r];
-    const T *z = (const T *)a.logits + r * a.stride;
-    const double inv = 1.0 / (double)tf, top = row.top;
+    const T *z = (const T *)a.logits + ((int64_t)b * a.rows + o.at) * a.stride;
+    const double inv = 1.0 / (double)tf, top = o.row.top;
     const float *q = claim_of(a, b, o.at, o.d);
-    const int32_t out = o.at < o.d && !q ? a.draft[(int64_t)b * (a.rows - 1) + o.at] : -1;
+    const int32_t out = q ? -1 : o.out;
     double total = 0.0;
     if (EXCESS) {
         double part = 0.0;
-        for (int32_t i = tid; i < draws; i += kThreads)
+        for (int32_t i = tid; i < draws; i += kDrawThreads)
             part += sp.weights[(int64_t)b * draws + i];
         total = block_sum(part, lds_d);
     }
     const float *over = EXCESS ? q : nullptr;
     const int32_t lo = piece * kDraw;
     double part = 0.0;
-#pragma unroll 4
+#pragma unroll
     for (int k = 0; k < kPer; ++k) {
-        const int32_t i = lo + k * kThreads + tid;
+        const int32_t i = lo + k * kDrawThreads + tid;
         if (i < a.vocab)
             part += weight_of(z, i, top, inv, out, over, total);
     }
@@ -485,24 +467,27 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
 
     // the last workgroup: the piece that holds the goal, then the token
     if (tid < kWave) {
-        const double u = a.uniform[(int64_t)b * a.rows + a.rows - 1];
-        double all = 0.0;
-        for (int32_t i = tid; i < draws; i += kWave)
+        double s = tid < draws ? peek(sums + tid) : 0.0;
+        double all = s;
+        for (int32_t i = tid + kWave; i < draws; i += kWave)
             all += peek(sums + i);
         all = wave_sum(all);
         if (EXCESS && !(all > 0.0)) {  // (then it is 0)
             // nothing exceeds q: draw from the weights
             over = nullptr;
             sums = sp.weights + (int64_t)b * draws;
-            for (int32_t i = tid; i < draws; i += kWave)
+            s = tid < draws ? peek(sums + tid) : 0.0;
+            all = s;
+            for (int32_t i = tid + kWave; i < draws; i += kWave)
                 all += peek(sums + i);
             all = wave_sum(all);
         }
-        const double goal = u * all;
+        const double goal = (double)o.u * all;
         double before = 0.0, at_before = 0.0;
         int32_t at = -1;
         for (int32_t base = 0; base < draws; base += kWave) {
-            const double s = base + tid < draws ? peek(sums + base + tid) : 0.0;
+            if (base > 0)
+                s = base + tid < draws ? peek(sums + base + tid) : 0.0;
             double run = s;  // inclusive
             for (int i = 1; i < kWave; i <<= 1) {
                 const double y = __shfl_up(run, i);
@@ -564,23 +549,27 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
             if (before > lds_goal && pick == 0x7fffffff)
                 pick = from + k;
         }
-    atomicMin(&lds_pick, pick);
-    atomicMax(&lds_last, last);
+    if (pick != 0x7fffffff)
+        atomicMin(&lds_pick, pick);
+    if (last >= 0)
+        atomicMax(&lds_last, last);
     __syncthreads();
     int32_t token = lds_pick != 0x7fffffff ? lds_pick : lds_last;
     if (token < 0)
         token = out >= 0 ? out : 0;  // no weight at all: the left-out token had it all
-    finish(a, sp, b, o, token,
-           (float)(((double)to_f32(z[token]) - top) * inv - log(row.total)));
+    if (tid == 0)
+        lds_z = to_f32(z[token]);
+    __syncthreads();
+    finish(a, sp, b, o, token, (float)(((double)lds_z - top) * inv - log(o.row.total)));
 }
 
 template <typename K>
-hipError_t start(K kernel, const VerifyArgs &a, const Space &sp, int64_t groups, int64_t pieces,
-                 hipStream_t s)
+hipError_t start(K kernel, int threads, const VerifyArgs &a, const Space &sp, int64_t groups,
+                 int64_t pieces, hipStream_t s)
 {
     if (groups * pieces > 0x7fffffffLL)
         return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(groups * pieces)), dim3(kThreads), 0, s, a, sp,
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(groups * pieces)), dim3(threads), 0, s, a, sp,
                        pieces);
     return hipGetLastError();
 }
@@ -591,15 +580,16 @@ hipError_t launch_typed(const VerifyArgs &a, hipStream_t s)
     const Space sp = space_of((char *)a.stats, a.max_batch, a.max_rows, a.vocab, nullptr);
     // 8,192 logits a piece, or 2,048 while that leaves the chip half empty
     constexpr int kWide = 8192 / (16 / sizeof(T)) / kThreads;
-    const int64_t rows = (int64_t)a.batch * a.rows;
-    hipError_t e = pieces_of(a.vocab, 8192) * rows >= 512
-                       ? start(stats_kernel<T, kWide>, a, sp, rows, pieces_of(a.vocab, 8192), s)
-                       : start(stats_kernel<T, kWide / 4>, a, sp, rows,
+    const int64_t rows = (int64_t)a.batch * a.rows, wide = pieces_of(a.vocab, 8192);
+    hipError_t e = wide * rows >= 512
+                       ? start(stats_kernel<T, kWide>, kThreads, a, sp, rows, wide, s)
+                       : start(stats_kernel<T, kWide / 4>, kThreads, a, sp, rows,
                                pieces_of(a.vocab, kMinPiece), s);
+    const int64_t draws = pieces_of(a.vocab, kDraw);
     if (e == hipSuccess)
-        e = start(draw_kernel<T, 0>, a, sp, a.batch, pieces_of(a.vocab, kDraw), s);
+        e = start(draw_kernel<T, 0>, kDrawThreads, a, sp, a.batch, draws, s);
     if (e == hipSuccess && a.head > 0)
-        e = start(draw_kernel<T, 1>, a, sp, a.batch, pieces_of(a.vocab, kDraw), s);
+        e = start(draw_kernel<T, 1>, kDrawThreads, a, sp, a.batch, draws, s);
     return e;
 }
 
