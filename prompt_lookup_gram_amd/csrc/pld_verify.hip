@@ -374,17 +374,20 @@ __device__ __forceinline__ Outcome outcome_of(const VerifyArgs &a, const Space &
     return o;
 }
 
-// Writes a request's outputs and clears its counters; the whole workgroup.
+// Writes a request's outputs but for the last token, and clears its
+// counters; the whole workgroup.
 __device__ __forceinline__ void finish(const VerifyArgs &a, const Space &sp, int32_t b,
-                                       const Outcome &o, int32_t token, float logp)
+                                       const Outcome &o)
 {
     const int64_t r = (int64_t)b * a.rows;
     for (int32_t t = threadIdx.x; t < a.rows; t += kDrawThreads) {
-        const bool in = !o.none && t <= o.at, drafted = in && t < o.at;
-        a.out_tokens[r + t] = drafted ? a.draft[(int64_t)b * (a.rows - 1) + t] : (in ? token : -1);
-        if (a.out_logprobs)
-            a.out_logprobs[r + t] = drafted ? sp.rows[r + t].logp : (in ? logp : 0.0f);
         sp.arrived[r + t] = 0;
+        if (!o.none && t == o.at)
+            continue;
+        const bool drafted = !o.none && t < o.at;
+        a.out_tokens[r + t] = drafted ? a.draft[(int64_t)b * (a.rows - 1) + t] : -1;
+        if (a.out_logprobs)
+            a.out_logprobs[r + t] = drafted ? sp.rows[r + t].logp : 0.0f;
     }
     if (threadIdx.x == 0) {
         a.out_accepted[b] = o.none ? 0 : o.at;
@@ -394,6 +397,15 @@ __device__ __forceinline__ void finish(const VerifyArgs &a, const Space &sp, int
         if (o.bad)
             atomicOr(a.err, (uint32_t)kErrBlock);
     }
+}
+
+// The last token; one thread.
+__device__ __forceinline__ void commit(const VerifyArgs &a, int32_t b, const Outcome &o,
+                                       int32_t token, double logp)
+{
+    a.out_tokens[(int64_t)b * a.rows + o.at] = token;
+    if (a.out_logprobs)
+        a.out_logprobs[(int64_t)b * a.rows + o.at] = (float)logp;
 }
 
 // Weight of token i of the row a request draws from: `out` is left out, and
@@ -418,7 +430,6 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
 {
     __shared__ double lds_d[kDrawWaves];
     __shared__ int32_t lds_say, lds_piece, lds_pick, lds_last;
-    __shared__ float lds_z;
     __shared__ double lds_before, lds_goal;
     const int32_t b = blockIdx.x / (uint32_t)draws, piece = blockIdx.x % (uint32_t)draws;
     const int32_t tid = threadIdx.x;
@@ -431,8 +442,11 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
     const Outcome o = outcome_of(a, sp, b);
     const float tf = temperature(a, b);
     if (o.none || tf == 0.0f) {
-        if (piece == 0)
-            finish(a, sp, b, o, o.row.arg, o.none ? 0.0f : (float)-log(o.row.total));
+        if (piece == 0) {
+            finish(a, sp, b, o);
+            if (!o.none && tid == 0)
+                commit(a, b, o, o.row.arg, -log(o.row.total));
+        }
         return;
     }
     const T *z = (const T *)a.logits + ((int64_t)b * a.rows + o.at) * a.stride;
@@ -466,6 +480,7 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
         return;
 
     // the last workgroup: the piece that holds the goal, then the token
+    finish(a, sp, b, o);
     if (tid < kWave) {
         double s = tid < draws ? peek(sums + tid) : 0.0;
         double all = s;
@@ -519,20 +534,21 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
     over = lds_say ? q : nullptr;
     const int32_t from = lds_piece * kDraw + tid * kPer;
     double w[kPer], run = 0.0;
+    float y[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-        w[k] = lds_piece >= 0 && from + k < a.vocab
-                   ? weight_of(z, from + k, top, inv, out, over, total)
-                   : 0.0;
+        const bool in = lds_piece >= 0 && from + k < a.vocab;
+        y[k] = in ? to_f32(z[from + k]) : 0.0f;
+        w[k] = in ? weight_of(z, from + k, top, inv, out, over, total) : 0.0;
         run += w[k];
     }
     // exclusive running sum over the threads
     double incl = run;
     const int lane = tid % kWave, wave = tid / kWave;
     for (int i = 1; i < kWave; i <<= 1) {
-        const double y = __shfl_up(incl, i);
+        const double x = __shfl_up(incl, i);
         if (lane >= i)
-            incl += y;
+            incl += x;
     }
     if (lane == kWave - 1)
         lds_d[wave] = incl;
@@ -541,26 +557,31 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
     for (int i = 0; i < wave; ++i)
         before += lds_d[i];
     int32_t pick = 0x7fffffff, last = -1;
+    float z_pick = 0.0f, z_last = 0.0f;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
         if (w[k] > 0.0) {
             before += w[k];
             last = from + k;
-            if (before > lds_goal && pick == 0x7fffffff)
+            z_last = y[k];
+            if (before > lds_goal && pick == 0x7fffffff) {
                 pick = from + k;
+                z_pick = y[k];
+            }
         }
     if (pick != 0x7fffffff)
         atomicMin(&lds_pick, pick);
     if (last >= 0)
         atomicMax(&lds_last, last);
     __syncthreads();
-    int32_t token = lds_pick != 0x7fffffff ? lds_pick : lds_last;
-    if (token < 0)
-        token = out >= 0 ? out : 0;  // no weight at all: the left-out token had it all
-    if (tid == 0)
-        lds_z = to_f32(z[token]);
-    __syncthreads();
-    finish(a, sp, b, o, token, (float)(((double)lds_z - top) * inv - log(o.row.total)));
+    // the thread that holds the token commits it; without any weight at all
+    // the token left out had it all
+    const int32_t token = lds_pick != 0x7fffffff ? lds_pick : lds_last;
+    if (token < 0 ? tid == 0 : (pick == token || (lds_pick == 0x7fffffff && last == token))) {
+        const int32_t x = token < 0 ? (out >= 0 ? out : 0) : token;
+        const float zx = token < 0 ? to_f32(z[x]) : (pick == token ? z_pick : z_last);
+        commit(a, b, o, x, ((double)zx - top) * inv - log(o.row.total));
+    }
 }
 
 template <typename K>
