@@ -37,10 +37,10 @@ namespace {
 constexpr int kWave = 64;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kDraw = 4096;                 // logits of a draw's piece
-constexpr int kDrawThreads = 512;
-constexpr int kDrawWaves = kDrawThreads / kWave;
-constexpr int kPer = kDraw / kDrawThreads;  // of a thread
+#ifndef BIGU
+#define BIGU (2 << 20)
+#endif
+constexpr int kMinUnit = 512;               // logits whose weights are summed together
 constexpr int32_t kNever = 0x7f7f7f7f;      // `stop` before a refusal
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr double kClear = 1.0 / 65536;      // relative distance that 32 bits decide
@@ -68,8 +68,8 @@ struct Row {
 struct Space {
     Piece *pieces;      // [batch * rows][pieces]
     Row *rows;          // [batch * rows]
-    double *weights;    // [batch][draws]: sums of a draw's pieces
-    double *excess;     // [batch][draws]: the same over q
+    double *weights;    // [batch][units]: sums of a row's weights
+    double *excess;     // [batch][units]: the same over q
     int32_t *arrived;   // [batch * rows], 0 between calls
     int32_t *drawn;     // [batch], 0 between calls
     int32_t *stop;      // [batch], kNever between calls
@@ -93,9 +93,9 @@ __host__ __device__ Space space_of(char *p, int64_t batch, int64_t rows, int32_t
     s.rows = (Row *)p;
     p += batch * rows * sizeof(Row);
     s.weights = (double *)p;
-    p += batch * pieces_of(vocab, kDraw) * sizeof(double);
+    p += batch * pieces_of(vocab, kMinUnit) * sizeof(double);
     s.excess = (double *)p;
-    p += batch * pieces_of(vocab, kDraw) * sizeof(double);
+    p += batch * pieces_of(vocab, kMinUnit) * sizeof(double);
     s.arrived = (int32_t *)p;
     p += batch * rows * sizeof(int32_t);
     s.drawn = (int32_t *)p;
@@ -380,7 +380,7 @@ __device__ __forceinline__ void finish(const VerifyArgs &a, const Space &sp, int
                                        const Outcome &o)
 {
     const int64_t r = (int64_t)b * a.rows;
-    for (int32_t t = threadIdx.x; t < a.rows; t += kDrawThreads) {
+    for (int32_t t = threadIdx.x; t < a.rows; t += kThreads) {
         sp.arrived[r + t] = 0;
         if (!o.none && t == o.at)
             continue;
@@ -408,31 +408,33 @@ __device__ __forceinline__ void commit(const VerifyArgs &a, int32_t b, const Out
         a.out_logprobs[(int64_t)b * a.rows + o.at] = (float)logp;
 }
 
-// Weight of token i of the row a request draws from: `out` is left out, and
-// with q only what exceeds it (scaled by the row's total) counts.
-template <typename T>
-__device__ __forceinline__ double weight_of(const T *z, int32_t i, double top, double inv,
+// Weight of token i, logit z, of the row a request draws from: `out` is left
+// out, and with q only what exceeds it (scaled by the row's total) counts.
+__device__ __forceinline__ double weight_of(float z, int32_t i, double top, double inv,
                                             int32_t out, const float *q, double total)
 {
-    const double w = i == out ? 0.0 : exp(((double)to_f32(z[i]) - top) * inv);
+    const double w = i == out ? 0.0 : exp(((double)z - top) * inv);
     if (!q)
         return w;
     const double e = w - (double)q[i] * total;
     return e > 0.0 ? e : 0.0;
 }
 
-// One workgroup per piece of a request's row to draw from. EXCESS 0: sums of
-// the weights; the last workgroup of a request without q at that row draws.
-// EXCESS 1 (a second launch, when there are drafter probabilities): sums of
-// the excess over q, whose total of the weights the first launch left.
-template <typename T, int EXCESS>
-__global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space sp, int32_t draws)
+// One wavefront per unit of 64 E logits of the row that a request draws from,
+// kWaves units a workgroup. EXCESS 0: sums of the weights; the last workgroup
+// of a request without q at that row draws. EXCESS 1 (a second launch, when
+// there are drafter probabilities): sums of the excess over q, whose total of
+// the weights the first launch left.
+template <typename T, int EXCESS, int E>
+__global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, int32_t groups)
 {
-    __shared__ double lds_d[kDrawWaves];
+    constexpr int N = 16 / sizeof(T), kUnit = E * kWave, kPer = kUnit / kThreads;
+    __shared__ double lds_d[kWaves];
     __shared__ int32_t lds_say, lds_piece, lds_pick, lds_last;
     __shared__ double lds_before, lds_goal;
-    const int32_t b = blockIdx.x / (uint32_t)draws, piece = blockIdx.x % (uint32_t)draws;
-    const int32_t tid = threadIdx.x;
+    const int32_t b = blockIdx.x / (uint32_t)groups, group = blockIdx.x % (uint32_t)groups;
+    const int32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int32_t draws = (int32_t)pieces_of(a.vocab, kUnit);
     if (EXCESS) {
         // requests that the first launch finished have cleared their row
         // counters; those left have row 0's
@@ -442,7 +444,7 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
     const Outcome o = outcome_of(a, sp, b);
     const float tf = temperature(a, b);
     if (o.none || tf == 0.0f) {
-        if (piece == 0) {
+        if (group == 0) {
             finish(a, sp, b, o);
             if (!o.none && tid == 0)
                 commit(a, b, o, o.row.arg, -log(o.row.total));
@@ -456,30 +458,53 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
     double total = 0.0;
     if (EXCESS) {
         double part = 0.0;
-        for (int32_t i = tid; i < draws; i += kDrawThreads)
+        for (int32_t i = tid; i < draws; i += kThreads)
             part += sp.weights[(int64_t)b * draws + i];
         total = block_sum(part, lds_d);
     }
     const float *over = EXCESS ? q : nullptr;
-    const int32_t lo = piece * kDraw;
-    double part = 0.0;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int32_t i = lo + k * kDrawThreads + tid;
-        if (i < a.vocab)
-            part += weight_of(z, i, top, inv, out, over, total);
-    }
-    part = block_sum(part, lds_d);
     double *sums = (EXCESS ? sp.excess : sp.weights) + (int64_t)b * draws;
-    if (tid == 0) {
-        poke(sums + piece, part);
-        lds_say = !EXCESS && q ? 0 : arrive(sp.drawn + b) == draws - 1;
+    const int32_t unit = group * kWaves + wave;
+    if (unit < draws) {
+        double part = 0.0;
+        const int32_t lo = unit * kUnit + lane * N;
+        float x[E];
+#pragma unroll
+        for (int w = 0; w < E / N; ++w) {
+            const int32_t i = lo + w * (kWave * N);
+            if (i <= a.vocab - N) {
+                const Word<T> y = *(const Word<T> *)(z + i);
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    x[w * N + k] = to_f32(y.x[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    x[w * N + k] = i + k < a.vocab ? to_f32(z[i + k]) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const int32_t i = lo + k / N * (kWave * N) + k % N;
+            if (i < a.vocab)
+                part += weight_of(x[k], i, top, inv, out, over, total);
+        }
+        part = wave_sum(part);
+        if (lane == 0) {
+            poke(sums + unit, part);
+            asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+        }
     }
+    __syncthreads();  // every wavefront's sum is stored
+    if (!EXCESS && q)
+        return;
+    if (tid == 0)
+        lds_say = arrive(sp.drawn + b) == groups - 1;
     __syncthreads();
     if (!lds_say)
         return;
 
-    // the last workgroup: the piece that holds the goal, then the token
+    // the last workgroup: the unit that holds the goal, then the token
     finish(a, sp, b, o);
     if (tid < kWave) {
         double s = tid < draws ? peek(sums + tid) : 0.0;
@@ -512,7 +537,7 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
             const unsigned long long over_goal = __ballot(s > 0.0 && before + run > goal);
             const unsigned long long live = __ballot(s > 0.0);
             if (live) {
-                // (the last piece with a weight stands in if rounding left none)
+                // (the last unit with a weight stands in if rounding left none)
                 const int k = over_goal ? __builtin_ctzll(over_goal) : 63 - __builtin_clzll(live);
                 at = base + k;
                 at_before = before + __shfl(run, k) - __shfl(s, k);
@@ -532,19 +557,18 @@ __global__ __launch_bounds__(kDrawThreads) void draw_kernel(VerifyArgs a, Space 
     }
     __syncthreads();
     over = lds_say ? q : nullptr;
-    const int32_t from = lds_piece * kDraw + tid * kPer;
+    const int32_t from = lds_piece * kUnit + tid * kPer;
     double w[kPer], run = 0.0;
     float y[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const bool in = lds_piece >= 0 && from + k < a.vocab;
         y[k] = in ? to_f32(z[from + k]) : 0.0f;
-        w[k] = in ? weight_of(z, from + k, top, inv, out, over, total) : 0.0;
+        w[k] = in ? weight_of(y[k], from + k, top, inv, out, over, total) : 0.0;
         run += w[k];
     }
     // exclusive running sum over the threads
     double incl = run;
-    const int lane = tid % kWave, wave = tid / kWave;
     for (int i = 1; i < kWave; i <<= 1) {
         const double x = __shfl_up(incl, i);
         if (lane >= i)
@@ -595,6 +619,17 @@ hipError_t start(K kernel, int threads, const VerifyArgs &a, const Space &sp, in
     return hipGetLastError();
 }
 
+template <typename T, int E>
+hipError_t launch_draw(const VerifyArgs &a, const Space &sp, hipStream_t s)
+{
+    const int64_t groups = pieces_of(a.vocab, E * kThreads);
+    const hipError_t e =
+        start(draw_kernel<T, 0, E>, kThreads, a, sp, a.batch, groups, s);
+    if (e != hipSuccess || a.head == 0)
+        return e;
+    return start(draw_kernel<T, 1, E>, kThreads, a, sp, a.batch, groups, s);
+}
+
 template <typename T>
 hipError_t launch_typed(const VerifyArgs &a, hipStream_t s)
 {
@@ -606,11 +641,10 @@ hipError_t launch_typed(const VerifyArgs &a, hipStream_t s)
                        ? start(stats_kernel<T, kWide>, kThreads, a, sp, rows, wide, s)
                        : start(stats_kernel<T, kWide / 4>, kThreads, a, sp, rows,
                                pieces_of(a.vocab, kMinPiece), s);
-    const int64_t draws = pieces_of(a.vocab, kDraw);
+    // units of 2,048 logits to draw from, or of 512 while they are few
     if (e == hipSuccess)
-        e = start(draw_kernel<T, 0>, kDrawThreads, a, sp, a.batch, draws, s);
-    if (e == hipSuccess && a.head > 0)
-        e = start(draw_kernel<T, 1>, kDrawThreads, a, sp, a.batch, draws, s);
+        e = (int64_t)a.batch * a.vocab >= BIGU ? launch_draw<T, 32>(a, sp, s)
+                                                  : launch_draw<T, 8>(a, sp, s);
     return e;
 }
 
