@@ -220,6 +220,10 @@ def parse():
     ap.add_argument("--append-draft", action="store_true",
                     help="workload 5 only: each step's append and the next step's draft "
                          "as one pld_append_draft_store call")
+    ap.add_argument("--verify-step", action="store_true",
+                    help="workload 5's start histories: time one verify step (the lookup "
+                         "draft, the block's keys and values into a paged cache, attention "
+                         "of the block, verification of the draft) instead of the drafting")
     ap.add_argument("--library-read", action="store_true",
                     help="also time torch.amax over the same rotated copies (a library "
                          "full read of the same bytes, for context)")
@@ -278,6 +282,12 @@ def main():
         print("--ngram drafts from the successor-count cache: it does not combine with "
               "--index or --fuse", file=sys.stderr)
         sys.exit(2)
+    if args.verify_step:
+        if args.config != 5 or args.index or args.ngram or args.fuse != "none" or args.control \
+                or args.append_draft:
+            print("--verify-step: workload 5 with scan drafting only", file=sys.stderr)
+            sys.exit(2)
+        return bench_verify_step(args, torch, B, wl, dev)
     if args.config == 5:
         return bench_stream(args, torch, B, wl, dev)
 
@@ -1025,6 +1035,123 @@ def bench_stream(args, torch, B, wl, dev):
         if mismatch is not None:
             print(json.dumps(rec))
             sys.exit(1)
+    print(json.dumps(rec), flush=True)
+
+
+# the verify step's geometry: one attention layer of a target model
+STEP_HEADS, STEP_KV_HEADS, STEP_DIM, STEP_PAGE, STEP_VOCAB = 32, 8, 128, 64, 151936
+
+
+def bench_verify_step(args, torch, B, wl, dev):
+    """One verify step of 64 requests at workload 5's start lengths, on fixed
+    histories: pld_draft_batch, then one layer's pld_kv_append and pld_attend
+    over a paged bf16 cache of random keys and values, then pld_verify on
+    random logits that hold the drafted tokens at a probability of about 0.8.
+    The calls are captured into one graph and replayed; each is also timed in
+    a graph of its own. Outputs of every replay equal the eager call's."""
+    start = wl.config5_start(args.stream_start or wl.STREAM_START_LEN)
+    nb, k, rows = start.batch, start.k_max, start.k_max + 1
+    hq, hk, dim, page, vocab = STEP_HEADS, STEP_KV_HEADS, STEP_DIM, STEP_PAGE, STEP_VOCAB
+    db = B.DeviceBatch(start.histories)
+    ctx = B.pld_create(nb, db.max_len)
+    p = B.pld_target_params_default()
+    p.max_batch, p.max_rows, p.max_len = nb, rows, db.max_len + k
+    p.q_heads, p.kv_heads, p.head_dim, p.page_tokens, p.vocab = hq, hk, dim, page, vocab
+    p.rope.rot_dim = dim
+    target = B.pld_create_target(p)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(11)
+    bf16, i32 = torch.bfloat16, torch.int32
+    width = -(-(db.max_len + k) // page)
+    pages = nb * width
+    table = torch.randperm(pages, generator=gen, device=dev).to(i32).view(nb, width)
+    kc = torch.empty((pages, hk, page, dim), dtype=bf16, device=dev)
+    vc = torch.empty((pages, hk, dim, page), dtype=bf16, device=dev)
+    for cells in (kc, vc):
+        for i in range(0, pages, 4096):
+            cells[i:i + 4096].normal_(generator=gen)
+    qkv = torch.randn((nb * rows, (hq + 2 * hk) * dim), generator=gen, device=dev).to(bf16)
+    q = torch.empty((nb * rows, hq * dim), dtype=bf16, device=dev)
+    attended = torch.zeros_like(q)
+    draft, dlen, match, _ = B.alloc_outputs(nb, k, device=dev)
+    uniform = torch.rand((nb, rows), generator=gen, device=dev)
+    tokens = torch.empty((nb, rows), dtype=i32, device=dev)
+    accepted, counts = (torch.empty(nb, dtype=i32, device=dev) for _ in range(2))
+    logits = torch.empty((nb, rows, vocab), dtype=bf16, device=dev)
+
+    def do_draft():
+        B.pld_draft_batch(ctx, db.rows, db.lengths, nb, start.n_min, start.n_max, k, draft, dlen,
+                          match)
+
+    def do_append():
+        w = qkv.shape[1]
+        B.pld_kv_append(target, qkv, w, qkv[:, hq * dim:], qkv[:, (hq + hk) * dim:], w, rows,
+                        db.lengths, dlen, nb, table, width, kc, vc, pages, None, None, q)
+
+    def do_attend():
+        B.pld_attend(target, q, hq * dim, rows, db.lengths, dlen, 0, nb, table, width, kc, vc,
+                     pages, None, None, 0.0, 0, attended)
+
+    def do_verify():
+        B.pld_verify(target, logits, vocab, rows, draft, dlen, None, None, 0, None, uniform, nb,
+                     tokens, accepted, counts)
+    do_draft()
+    for b in range(nb):
+        z = torch.randn((rows, vocab), generator=gen, device=dev) * 2.0
+        x = draft[b].clamp(min=0).long()[:, None]
+        z[:k].scatter_(1, x, torch.logsumexp(z[:k], 1, keepdim=True) + 1.4)
+        logits[b] = z.to(bf16)
+    steps = {"draft": do_draft, "kv_append": do_append, "attend": do_attend, "verify": do_verify}
+
+    def do_step():
+        for f in steps.values():
+            f()
+    do_step()
+    assert B.pld_sync(ctx) == B.PLD_OK and B.pld_sync(target) == B.PLD_OK
+    want = [t.clone() for t in (attended, tokens, accepted)]
+
+    def timed(f, reps):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            f()
+        for _ in range(max(1, args.warmup if reps == args.steps else 3)):
+            graph.replay()
+        torch.cuda.synchronize()
+        e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        t0 = time.perf_counter()
+        e0.record()
+        for _ in range(reps):
+            graph.replay()
+        e1.record()
+        torch.cuda.synchronize()
+        wall = time.perf_counter() - t0
+        for a_, b_ in zip(want, (attended, tokens, accepted)):
+            assert torch.equal(a_, b_), "graph replay differs from the eager pass"
+        return wall, e0.elapsed_time(e1) * 1e-3
+    wall, gpu_s = timed(do_step, args.steps)
+    part = {name: timed(f, min(200, args.steps))[1] / min(200, args.steps) * 1e6
+            for name, f in steps.items()}
+    assert B.pld_sync(ctx) == B.PLD_OK and B.pld_sync(target) == B.PLD_OK
+    seen = int((db.lengths + dlen).sum())
+    cache_bytes = seen * hk * dim * 2 * 2
+    rec = {
+        "metric": "verify steps/s; us per call of the step",
+        "value": round(args.steps / wall, 1), "unit": "verify steps/s", "n_gpus": 1,
+        "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(wall * 1e3 / args.steps, 6), "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": start.name, "batch": nb, "q_heads": hq, "kv_heads": hk,
+                   "head_dim": dim, "page_tokens": page, "vocab": vocab, "rows": rows,
+                   "layers": 1, "mean_draft": round(float(dlen.float().mean()), 2),
+                   "mean_accepted": round(float(accepted.float().mean()), 2)},
+        "us_per_step": round(gpu_s * 1e6 / args.steps, 2),
+        "us_per_call": {n: round(t, 2) for n, t in part.items()},
+        "attend_cache_GBps": round(cache_bytes / part["attend"] / 1e3, 1),
+        "time_source": "value, ms_per_step: host clock around the replays, a device synchronize "
+                       "on each side; us_*: HIP events on the launch stream",
+    }
+    B.pld_destroy(ctx)
+    B.pld_destroy(target)
     print(json.dumps(rec), flush=True)
 
 

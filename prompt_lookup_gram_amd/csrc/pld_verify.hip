@@ -37,9 +37,6 @@ namespace {
 constexpr int kWave = 64;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-#ifndef BIGU
-#define BIGU (2 << 20)
-#endif
 constexpr int kMinUnit = 512;               // logits whose weights are summed together
 constexpr int32_t kNever = 0x7f7f7f7f;      // `stop` before a refusal
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -643,8 +640,8 @@ hipError_t launch_typed(const VerifyArgs &a, hipStream_t s)
                                pieces_of(a.vocab, kMinPiece), s);
     // units of 2,048 logits to draw from, or of 512 while they are few
     if (e == hipSuccess)
-        e = (int64_t)a.batch * a.vocab >= BIGU ? launch_draw<T, 32>(a, sp, s)
-                                                  : launch_draw<T, 8>(a, sp, s);
+        e = (int64_t)a.batch * a.vocab >= (2 << 20) ? launch_draw<T, 32>(a, sp, s)
+                                                     : launch_draw<T, 8>(a, sp, s);
     return e;
 }
 
