@@ -18,8 +18,10 @@
 //  - the 32-bit sum decides only where it is clear. Its relative error is
 //    below 32 * 2^-23 (the arguments' rounding, weighed by the softmax, is at
 //    most ln V * 2^-23 for V < 2^18, the function's and the additions' the
-//    rest), so within 2^-16 of the edge the deciding workgroup sums the row
-//    again in 64 bits.
+//    rest). Within 2^-17 of the edge (one decision in 65,000) the deciding
+//    wavefront sums the row again with 64-bit arguments and sums, which
+//    leaves the function's 2^-23 (75 us for 151,936 logits), and within 2^-22
+//    with 64-bit exponentials as well (430 us).
 // Numbers that cross workgroups do so in relaxed agent-scope atomics, each
 // performed at the point of coherence; a workgroup waits for its stores to
 // complete before it counts itself in, so who counts last reads them all.
@@ -40,7 +42,9 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMinUnit = 512;               // logits whose weights are summed together
 constexpr int32_t kNever = 0x7f7f7f7f;      // `stop` before a refusal
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr double kClear = 1.0 / 65536;      // relative distance that 32 bits decide
+constexpr double kLog2e64 = 1.4426950408889634074;
+constexpr double kClear = 1.0 / (1 << 17);  // relative distances that the 32-bit sum
+constexpr double kClearer = 1.0 / (1 << 22);  // and the one after it decide
 
 // A piece of a row: the largest logit, the sum of exp((z - top) / T) (NaN
 // when it holds NaN or +inf), and the lowest index of the largest (greedy).
@@ -169,9 +173,43 @@ __device__ __forceinline__ const float *claim_of(const VerifyArgs &a, int32_t b,
     return a.probs + ((int64_t)b * a.head + t) * a.vocab;
 }
 
+// sum exp((z - m) inv) over a row by one wavefront, to 2^-22: 2^y with y in 64
+// bits, its whole part split off before the 32-bit function.
+template <typename T>
+__device__ __forceinline__ double sum_again(const T *z, int32_t vocab, float m, double inv, int lane)
+{
+    constexpr int N = 16 / sizeof(T), kDeep = 4;
+    const double c = inv * kLog2e64, base = (double)m * c;
+    double sum = 0.0;
+    const auto add = [&](float x) {
+        const double y = fma((double)x, c, -base), n = rint(y);
+        // (below 2^-149 the weight is 0, the whole part may be -infinity)
+        if (n > -150.0)
+            sum += (double)ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
+    };
+    int32_t i = lane * N;
+    for (; i <= vocab - (kDeep - 1) * kWave * N - N; i += kDeep * kWave * N) {
+        Word<T> w[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+            w[k] = *(const Word<T> *)(z + i + k * kWave * N);
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                add(to_f32(w[k].x[e]));
+    }
+    for (; i < vocab; i += kWave * N)
+        for (int e = 0; e < N && i + e < vocab; ++e)
+            add(to_f32(z[i + e]));
+    return wave_sum(sum);
+}
+
 // One workgroup per piece of a row, W 16-byte words a thread.
+// (8 wavefronts a SIMD: the rare second sum must not cost the first its
+// registers)
 template <typename T, int W>
-__global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a, Space sp, uint32_t pieces)
+__global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Space sp, uint32_t pieces)
 {
     constexpr int N = 16 / sizeof(T);
     constexpr int kPiece = W * N * kThreads;
@@ -304,10 +342,14 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a, Space sp,
         const double zx = ((double)z_token - m) * inv, p = exp(zx) / total;
         logp = (float)(zx - log(total));
         if (!greedy && fabs(weight - p) <= kClear * p) {
-            double sure = 0.0;
-            for (int32_t i = lane; i < a.vocab; i += kWave)
-                sure += exp(((double)to_f32(z[i]) - m) * inv);
-            say = weight < exp(zx) / wave_sum(sure) ? kAccept : kRefuse;
+            double sure = exp(zx) / sum_again(z, a.vocab, m, inv, lane);
+            if (fabs(weight - sure) <= kClearer * sure) {
+                double all = 0.0;
+                for (int32_t i = lane; i < a.vocab; i += kWave)
+                    all += exp(((double)to_f32(z[i]) - m) * inv);
+                sure = exp(zx) / wave_sum(all);
+            }
+            say = weight < sure ? kAccept : kRefuse;
         } else {
             say = (greedy ? token == best : weight < p) ? kAccept : kRefuse;
         }

@@ -247,6 +247,27 @@ def test_acceptance_next_to_its_edge():
         B.pld_destroy(ctx)
 
 
+@pytest.mark.parametrize("dt,vocab", [("bf16", 151936), ("f32", 50257), ("f16", 700)])
+@pytest.mark.parametrize("rel", [2.0**-24, 2.0**-21, 2.0**-18, 2.0**-15])
+def test_acceptance_at_distances_that_take_different_sums(dt, vocab, rel):
+    """u a given relative distance off p(x), above and below: the 32-bit sum,
+    the one with 64-bit arguments and the 64-bit one agree on the side."""
+    c = Case(4, 2, vocab, dt=dt, seed=18, accept=0.5)
+    for b in range(4):
+        e = np.exp(c.z[b, 0] - c.z[b, 0].max())
+        c.uniform[b, 0] = e[c.draft[b, 0]] / e.sum() * (1 + rel * (-1) ** b)
+    ctx = context(4, 2, vocab)
+    try:
+        out = c.outputs()
+        B.pld_verify(ctx, *c.args(), *out)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        acc = c.compare(out)
+        if rel > 2.0**-22:  # (past the rounding of u itself)
+            assert acc.tolist() == [0, 1, 0, 1]
+    finally:
+        B.pld_destroy(ctx)
+
+
 def test_drafter_equal_to_target_is_always_accepted_and_zero_excess_draws_from_p():
     import torch
     c = Case(8, 3, 256, seed=14, head=2)
