@@ -638,8 +638,9 @@ typedef struct pld_rope_params {
 
 typedef struct pld_target_params {
     int32_t max_batch;   /* requests a call may hold, >= 1 */
-    int32_t max_rows;    /* rows of a padded block, >= 1 */
-    int64_t max_len;     /* largest L + d, as pld_create's max_len */
+    int32_t max_rows;    /* rows of a padded block, >= 1; times max_batch or
+                            q_heads / kv_heads at most 2^30 */
+    int64_t max_len;     /* largest L + d, 1 .. 2^30 */
     int32_t q_heads;     /* a multiple of kv_heads; 0 with kv_heads 0: a context
                             for pld_verify alone */
     int32_t kv_heads;
@@ -647,7 +648,7 @@ typedef struct pld_target_params {
     int32_t dtype;       /* q, k, v and outputs: PLD_F16 or PLD_BF16 */
     int32_t cache_dtype; /* the cache: dtype or PLD_E4M3 */
     int32_t page_tokens; /* 16, 32, 64, 128 or 256 */
-    int32_t vocab;       /* of pld_verify; 0: a context without it */
+    int32_t vocab;       /* of pld_verify, at most 2^24; 0: a context without it */
     pld_rope_params rope;
 } pld_target_params;
 
@@ -678,7 +679,7 @@ pld_status pld_create_target(pld_ctx **out, const pld_target_params *params,
  *  v_cache: device cache_dtype [n_pages][kv_heads][head_dim][page_tokens]
  * both 16-byte aligned. V lies with its positions side by side: the matrix
  * instructions that sum probabilities times V take it as it is loaded.
- *  k_scale, v_scale: device float[kv_heads] or NULL (1): with an E4M3 cache a
+ *  k_scale, v_scale: device float[kv_heads], positive, or NULL (1): with an E4M3 cache a
  *  cell holds value / scale, rounded, at most 448 in magnitude. Not used
  *  with a 16-bit cache.
  * table_stride >= 1 is also the number of entries a table row holds. A page id
@@ -782,7 +783,8 @@ pld_status pld_attend(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t row
  *  draft_probs, head: device float [batch][head][vocab], the drafter's
  *            probabilities at positions 0..head-1, or NULL with head 0;
  *            0 <= head <= rows - 1.
- *  temperature: device float[batch], >= 0 and finite, or NULL: 1 throughout.
+ *  temperature: device float[batch], 0 or a normal positive number, or NULL: 1
+ *            throughout.
  *  uniform:  device float [batch][rows], values in [0, 1): column t < rows - 1
  *            decides draft position t, the last column draws the token.
  *  out_tokens: device int32 [batch][rows]: the committed tokens, -1 past them
@@ -794,8 +796,8 @@ pld_status pld_attend(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t row
  * d = -1: no tokens, a = 0 and count 0. Rows after a refusal need not be
  * read and are not checked. A request is written like d = -1 and sets the
  * sticky flag (PLD_EINVAL) when d is outside its range, a draft token before d
- * outside the vocabulary, T negative or not finite, a uniform it may use
- * outside [0, 1), or a row it needs holds NaN, +inf or only -inf.
+ * outside the vocabulary, T negative, subnormal or not finite, a uniform it may
+ * use outside [0, 1), or a row it needs holds NaN, +inf or only -inf.
  * Errors: PLD_EINVAL, PLD_EHIP.
  */
 pld_status pld_verify(pld_ctx *ctx, const void *logits, int32_t logits_dtype,

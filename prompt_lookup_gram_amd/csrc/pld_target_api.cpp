@@ -34,6 +34,8 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 constexpr int kMaxPairs = 128;  // head_dim 256
+constexpr int64_t kMost = 1 << 30;
+constexpr int32_t kMaxVocab = 1 << 24;
 
 // Turns (angle / 2 pi) per position of each rotated pair, in 64 bits.
 void rope_turns(const pld_rope_params &r, double *turns)
@@ -70,12 +72,13 @@ pld_status check_params(const pld_target_params &p)
         return fail(PLD_EINVAL, "max_batch must be >= 1 (got %d)", p.max_batch);
     if (p.max_rows < 1)
         return fail(PLD_EINVAL, "max_rows must be >= 1 (got %d)", p.max_rows);
-    if (p.max_len < 1 || p.max_len > 0x7fffffffLL)
-        return fail(PLD_EINVAL, "max_len must be in [1, 2^31-1] (got %lld)", (long long)p.max_len);
-    if ((int64_t)p.max_batch * p.max_rows > 0x7fffffffLL)
-        return fail(PLD_EINVAL, "max_batch * max_rows must be below 2^31");
-    if (p.vocab < 0)
-        return fail(PLD_EINVAL, "vocab must be >= 0 (got %d)", p.vocab);
+    // (the kernels step past the last position, row and logit in 32 bits)
+    if (p.max_len < 1 || p.max_len > kMost)
+        return fail(PLD_EINVAL, "max_len must be in [1, 2^30] (got %lld)", (long long)p.max_len);
+    if ((int64_t)p.max_batch * p.max_rows > kMost)
+        return fail(PLD_EINVAL, "max_batch * max_rows must be at most 2^30");
+    if (p.vocab < 0 || p.vocab > kMaxVocab)
+        return fail(PLD_EINVAL, "vocab must be in [0, 2^24] (got %d)", p.vocab);
     if (p.q_heads < 0 || p.kv_heads < 0 || (p.q_heads == 0) != (p.kv_heads == 0) ||
         (p.kv_heads > 0 && p.q_heads % p.kv_heads != 0) || p.q_heads > 65536)
         return fail(PLD_EINVAL, "q_heads must be a multiple of kv_heads, at most 65536 "
@@ -84,6 +87,8 @@ pld_status check_params(const pld_target_params &p)
         return fail(PLD_EINVAL, "a target context needs heads or a vocab");
     if (p.q_heads == 0)
         return PLD_OK;
+    if ((int64_t)p.max_rows * (p.q_heads / p.kv_heads) > kMost)
+        return fail(PLD_EINVAL, "max_rows * q_heads / kv_heads must be at most 2^30");
     if (p.head_dim != 64 && p.head_dim != 96 && p.head_dim != 128 && p.head_dim != 192 &&
         p.head_dim != 256)
         return fail(PLD_EINVAL, "head_dim %d not one of 64, 96, 128, 192, 256", p.head_dim);

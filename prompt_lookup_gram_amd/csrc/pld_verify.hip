@@ -16,9 +16,9 @@
 //    that is known (`stop`). What is skipped never changes a result: only
 //    rows up to the first refusal are looked at;
 //  - the 32-bit sum decides only where it is clear. Its relative error is
-//    below 32 * 2^-23 (the arguments' rounding, weighed by the softmax, is at
-//    most ln V * 2^-23 for V < 2^18, the function's and the additions' the
-//    rest). Within 2^-17 of the edge (one decision in 65,000) the deciding
+//    below 48 * 2^-23: an argument y is off by 1.5 * 2^-23 |y|, which the
+//    softmax weighs to at most 1.5 ln V * 2^-23 = 25 * 2^-23 for V <= 2^24, the
+//    function by 2^-23, 40 additions by 20 * 2^-23. Within 2^-17 of the edge (one decision in 65,000) the deciding
 //    wavefront sums the row again with 64-bit arguments and sums, which
 //    leaves the function's 2^-23 (75 us for 151,936 logits), and within 2^-22
 //    with 64-bit exponentials as well (430 us).
@@ -27,6 +27,7 @@
 // complete before it counts itself in, so who counts last reads them all.
 
 #include <hip/hip_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -179,10 +180,10 @@ template <typename T>
 __device__ __forceinline__ double sum_again(const T *z, int32_t vocab, float m, double inv, int lane)
 {
     constexpr int N = 16 / sizeof(T), kDeep = 4;
-    const double c = inv * kLog2e64, base = (double)m * c;
+    const double c = inv * kLog2e64;
     double sum = 0.0;
     const auto add = [&](float x) {
-        const double y = fma((double)x, c, -base), n = rint(y);
+        const double y = ((double)x - m) * c, n = rint(y);
         // (below 2^-149 the weight is 0, the whole part may be -infinity)
         if (n > -150.0)
             sum += (double)ldexpf(__builtin_amdgcn_exp2f((float)(y - n)), (int)n);
@@ -263,14 +264,21 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Space 
 #pragma unroll
     for (int w = 1; w < kWaves; ++w)
         top = fmaxf(top, lds_max[w]);
-    // (without a finite logit the sum is 0, or NaN with a NaN; what rounding
-    // took off the common exponent is put back into the sum)
-    const float base = top == -INFINITY ? 0.0f : top * c;
-    const float rest = top == -INFINITY ? 0.0f : fmaf(top, c, -base);
-    float sum = 0.0f;
+    // (without a finite logit the sum is 0, or NaN with a NaN.) One operation a
+    // logit where what rounding takes off the common exponent is small enough
+    // to be put back into the sum; far logits take two.
+    float base = top * c, rest = 0.0f, sum = 0.0f;
+    if (fabsf(base) < 1048576.0f) {
+        rest = fmaf(top, c, -base);
 #pragma unroll
-    for (int k = 0; k < W * N; ++k)
-        sum += __builtin_amdgcn_exp2f(fmaf(x[k], c, -base));
+        for (int k = 0; k < W * N; ++k)
+            sum += __builtin_amdgcn_exp2f(fmaf(x[k], c, -base));
+    } else {
+        base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int k = 0; k < W * N; ++k)
+            sum += __builtin_amdgcn_exp2f((x[k] - base) * c);
+    }
     sum = wave_sum(sum);
     int32_t arg = 0x7fffffff;
     if (greedy) {
@@ -382,7 +390,7 @@ __device__ __forceinline__ Outcome outcome_of(const VerifyArgs &a, const Space &
     o.u = a.uniform[r + a.rows - 1];
     const float tf = temperature(a, b);
     const bool greedy = tf == 0.0f;
-    bool bad = !(tf >= 0.0f) || tf == INFINITY || o.d < -1 || o.d >= a.rows;
+    bool bad = !(greedy || (tf >= FLT_MIN && tf <= FLT_MAX)) || o.d < -1 || o.d >= a.rows;
     o.at = o.d;
     o.out = -1;
     o.row = Row{};

@@ -136,6 +136,16 @@ def test_types_and_head_dims(dt, cache, dim, rows):
           seed=dim + rows)
 
 
+@pytest.mark.parametrize("dt,cache", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3"),
+                                      ("f16", "e4m3")])
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("rows", [6, 10, 20, 40])
+def test_types_and_head_dims_with_more_query_rows(dt, cache, dim, rows):
+    # 24, 40, 80 and 160 query rows a kv head, spans joined (700 positions)
+    check([1, 77, 700, 0], [rows - 1, 3, rows - 2, 5], rows, hq=8, hk=2, dim=dim, dt=dt,
+          cache=cache, page=32, window=0 if dim != 128 else 90, seed=dim + rows)
+
+
 @pytest.mark.parametrize("hq,hk", [(1, 1), (2, 2), (3, 1), (8, 2), (12, 2), (16, 1), (7, 1),
                                    (32, 2), (40, 1)])
 @pytest.mark.parametrize("rows", [1, 2, 9])
@@ -413,6 +423,39 @@ def test_repeated_calls_are_bit_identical_and_graphs_replay():
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     finally:
         B.pld_destroy(ctx)
+
+
+def test_two_contexts_on_two_streams_at_once():
+    """Each context's workspace is its own: calls overlapping on two streams
+    give what they give one after the other; inputs are made on the stream
+    that uses them."""
+    import torch
+    cases = [Case([6000, 300], [3, 3], 4, hq=8, hk=2, dim=128, page=64, seed=15),
+             Case([9000, 5], [15, 0], 16, hq=8, hk=1, dim=64, page=16, seed=16)]
+    ctxs = [c.context() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    try:
+        want = []
+        for c, ctx in zip(cases, ctxs):
+            want.append(c.outputs())
+            c.call(ctx, *want[-1])
+            assert B.pld_sync(ctx) == B.PLD_OK
+        torch.cuda.synchronize()
+        got = [[], []]
+        for _ in range(8):
+            for i, (c, ctx, st) in enumerate(zip(cases, ctxs, streams)):
+                with torch.cuda.stream(st):
+                    got[i].append(c.outputs())
+                    B.pld_attend(ctx, c.q, c.width, c.rows, c.ln, c.dl, 0, c.b, c.tab,
+                                 c.tab.shape[1], c.kc, c.vc, c.pages, None, None, 0.0, 0,
+                                 *got[i][-1])
+        for i in range(2):
+            assert B.pld_sync(ctxs[i], streams[i]) == B.PLD_OK
+            for out in got[i]:
+                assert torch.equal(out[0], want[i][0]) and torch.equal(out[1], want[i][1])
+    finally:
+        for ctx in ctxs:
+            B.pld_destroy(ctx)
 
 
 def test_refusals_on_a_context():

@@ -38,7 +38,8 @@ def test_defaults():
 
 @pytest.mark.parametrize("field,value,word", [
     ("max_batch", 0, "max_batch"), ("max_rows", 0, "max_rows"), ("max_len", 0, "max_len"),
-    ("max_len", 2**31, "max_len"), ("vocab", -1, "vocab"), ("q_heads", 7, "q_heads"),
+    ("max_len", 2**30 + 1, "max_len"), ("vocab", -1, "vocab"), ("vocab", 2**24 + 1, "vocab"),
+    ("max_batch", 2**27, "max_batch"), ("max_rows", 2**29, "max_rows"), ("q_heads", 7, "q_heads"),
     ("q_heads", 0, "q_heads"), ("kv_heads", 0, "q_heads"), ("kv_heads", -2, "q_heads"),
     ("head_dim", 80, "head_dim"), ("head_dim", 512, "head_dim"), ("dtype", B.PLD_F32, "dtype"),
     ("dtype", 9, "dtype"), ("cache_dtype", B.PLD_F16, "cache_dtype"),
