@@ -499,36 +499,64 @@ def pld_append_draft_ngram(ctx: int, tokens, tokens_stride: int, counts, batch: 
         _stream(stream)))
 
 
-def _rows_ptr(x, name: str, dtypes):
-    """Device pointer of rows at a stride: a GPU tensor (or a slice of one)
-    whose last dimension is dense, of one of `dtypes`; or a raw pointer."""
-    if x is None:
-        return 0
-    if isinstance(x, int):
-        return x
-    import torch
-    if not isinstance(x, torch.Tensor):
+# The verify step's calls take many tensors and are small: their checks are
+# one pass over each tensor, with the dtypes looked up once.
+_types = None
+
+
+def _verify_types():
+    global _types
+    if _types is None:
+        import torch
+        half = (torch.float16, torch.bfloat16)
+        _types = {"tensor": torch.Tensor, "i32": (torch.int32,),
+                  "i64": (torch.int64,), "f32": (torch.float32,), "half": half,
+                  "cells": half + (torch.float8_e4m3fn,),
+                  "logits": {torch.float32: PLD_F32, torch.float16: PLD_F16,
+                             torch.bfloat16: PLD_BF16},
+                  "device": torch.cuda.current_device, "gpu": torch.cuda.is_available()}
+    return _types
+
+
+def _refuse(x, name: str, dtypes, device: int, rows: bool):
+    """The error of a tensor that _arg does not take."""
+    if not hasattr(x, "data_ptr"):
         raise TypeError(f"{name}: expected a torch tensor or a device pointer")
     if x.device.type != "cuda":
         raise ValueError(f"{name}: tensor must be on the GPU (got {x.device})")
-    if x.numel() and x.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension must be dense (stride {x.stride(-1)})")
     if x.dtype not in dtypes:
         raise ValueError(f"{name}: dtype must be one of {tuple(dtypes)} (got {x.dtype})")
-    return x.data_ptr()
+    if x.get_device() != device:
+        raise ValueError(f"{name}: tensor is on {x.device}, the current device is cuda:{device}")
+    if rows:
+        raise ValueError(f"{name}: the last dimension must be dense (stride {x.stride(-1)})")
+    raise ValueError(f"{name}: tensor must be contiguous")
 
 
-def _same_device(**tensors) -> None:
-    """Every tensor lies on the current device, whose stream the call takes."""
-    import torch
-    current = None
-    for name, x in tensors.items():
-        if isinstance(x, torch.Tensor) and x.device.type == "cuda":
-            if current is None:
-                current = torch.cuda.current_device()
-            if x.device.index != current:
-                raise ValueError(f"{name}: tensor is on {x.device}, the current device is "
-                                 f"cuda:{current}")
+def _arg(x, name: str, dtypes, device: int):
+    """Device pointer of a contiguous tensor of one of `dtypes` on the
+    current device, or of a raw pointer; None for None."""
+    if x is None or x.__class__ is int:
+        return x
+    if (isinstance(x, _types["tensor"]) and x.get_device() == device and x.dtype in dtypes
+            and x.is_contiguous()):
+        return x.data_ptr()
+    return _refuse(x, name, dtypes, device, False)
+
+
+def _rows_arg(x, name: str, dtypes, device: int):
+    """_arg for rows at a stride: only the last dimension must be dense."""
+    if x is None or x.__class__ is int:
+        return x
+    if (isinstance(x, _types["tensor"]) and x.get_device() == device and x.dtype in dtypes
+            and (x.is_contiguous() or x.stride(-1) == 1)):
+        return x.data_ptr()
+    return _refuse(x, name, dtypes, device, True)
+
+
+def _device(t) -> int:
+    """The current device; without a GPU a number that no tensor's is."""
+    return t["device"]() if t["gpu"] else -2
 
 
 def pld_target_params_default() -> PldTargetParams:
@@ -551,26 +579,17 @@ def pld_kv_append(ctx: int, q, q_stride: int, k, v, kv_stride: int, rows: int, l
     """Rotary positions, and the block's keys and values into the paged
     cache (include/pld.h). q, k and v may be slices whose rows lie q_stride
     and kv_stride elements apart."""
-    import torch
-    i32, half = _i32(), (torch.float16, torch.bfloat16)
-    cell = half + (torch.float8_e4m3fn,)
-    _same_device(q=q, k=k, v=v, lengths=lengths, draft_len=draft_len, page_table=page_table,
-                 k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out_q=out_q)
-    _check("pld_kv_append", load().pld_kv_append(
-        ctx, _rows_ptr(q, "q", half), int(q_stride), _rows_ptr(k, "k", half),
-        _rows_ptr(v, "v", half), int(kv_stride), int(rows), _dev_ptr(lengths, "lengths", i32),
-        _dev_ptr(draft_len, "draft_len", i32), int(batch),
-        _dev_ptr(page_table, "page_table", i32), int(table_stride),
-        _cells(k_cache, "k_cache", cell), _cells(v_cache, "v_cache", cell), int(n_pages),
-        _dev_ptr(k_scale, "k_scale", torch.float32), _dev_ptr(v_scale, "v_scale", torch.float32),
-        _cells(out_q, "out_q", half), _stream(stream)))
-
-
-def _cells(x, name: str, dtypes) -> int:
-    """_dev_ptr of a contiguous buffer of one of `dtypes`."""
-    if x is not None and not isinstance(x, int) and getattr(x, "dtype", None) not in dtypes:
-        raise ValueError(f"{name}: dtype must be one of {tuple(dtypes)}")
-    return _dev_ptr(x, name)
+    t = _types or _verify_types()
+    dev, i32, half, cells, f32 = _device(t), t["i32"], t["half"], t["cells"], t["f32"]
+    st = (_lib or load()).pld_kv_append(
+        ctx, _rows_arg(q, "q", half, dev), q_stride, _rows_arg(k, "k", half, dev),
+        _rows_arg(v, "v", half, dev), kv_stride, rows, _arg(lengths, "lengths", i32, dev),
+        _arg(draft_len, "draft_len", i32, dev), batch, _arg(page_table, "page_table", i32, dev),
+        table_stride, _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev),
+        n_pages, _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev),
+        _arg(out_q, "out_q", half, dev), _stream(stream))
+    if st:
+        _check("pld_kv_append", st)
 
 
 def pld_attend(ctx: int, q, q_stride: int, rows: int, lengths, draft_len, max_len: int,
@@ -578,20 +597,17 @@ def pld_attend(ctx: int, q, q_stride: int, rows: int, lengths, draft_len, max_le
                k_scale=None, v_scale=None, scale: float = 0.0, window: int = 0, out=None,
                out_lse=None, stream=None) -> None:
     """Attention of the block's rows over the paged cache (include/pld.h)."""
-    import torch
-    i32, half = _i32(), (torch.float16, torch.bfloat16)
-    cell = half + (torch.float8_e4m3fn,)
-    _same_device(q=q, lengths=lengths, draft_len=draft_len, page_table=page_table,
-                 k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=out,
-                 out_lse=out_lse)
-    _check("pld_attend", load().pld_attend(
-        ctx, _rows_ptr(q, "q", half), int(q_stride), int(rows),
-        _dev_ptr(lengths, "lengths", i32), _dev_ptr(draft_len, "draft_len", i32), int(max_len),
-        int(batch), _dev_ptr(page_table, "page_table", i32), int(table_stride),
-        _cells(k_cache, "k_cache", cell), _cells(v_cache, "v_cache", cell), int(n_pages),
-        _dev_ptr(k_scale, "k_scale", torch.float32), _dev_ptr(v_scale, "v_scale", torch.float32),
-        float(scale), int(window), _cells(out, "out", half),
-        _dev_ptr(out_lse, "out_lse", torch.float32), _stream(stream)))
+    t = _types or _verify_types()
+    dev, i32, half, cells, f32 = _device(t), t["i32"], t["half"], t["cells"], t["f32"]
+    st = (_lib or load()).pld_attend(
+        ctx, _rows_arg(q, "q", half, dev), q_stride, rows, _arg(lengths, "lengths", i32, dev),
+        _arg(draft_len, "draft_len", i32, dev), max_len, batch,
+        _arg(page_table, "page_table", i32, dev), table_stride,
+        _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev), n_pages,
+        _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev), scale, window,
+        _arg(out, "out", half, dev), _arg(out_lse, "out_lse", f32, dev), _stream(stream))
+    if st:
+        _check("pld_attend", st)
 
 
 def pld_verify(ctx: int, logits, logits_stride: int, rows: int, draft, draft_len, src,
@@ -601,24 +617,21 @@ def pld_verify(ctx: int, logits, logits_stride: int, rows: int, draft, draft_len
     (or a slice of one) whose rows lie logits_stride elements apart; its
     dtype is the call's logits_dtype. `src` is an int64 tensor of bit masks
     or None, `temperature` a float32 tensor or None (1 throughout)."""
-    import torch
-    i32, f32 = _i32(), torch.float32
-    types = {torch.float32: PLD_F32, torch.float16: PLD_F16, torch.bfloat16: PLD_BF16}
-    if not isinstance(logits, torch.Tensor):
+    t = _types or _verify_types()
+    dev, i32, f32, types = _device(t), t["i32"], t["f32"], t["logits"]
+    if not isinstance(logits, t["tensor"]):
         raise TypeError("logits: expected a torch tensor")
-    _same_device(logits=logits, draft=draft, draft_len=draft_len, src=src,
-                 draft_probs=draft_probs, temperature=temperature, uniform=uniform,
-                 out_tokens=out_tokens, out_accepted=out_accepted, out_counts=out_counts,
-                 out_logprobs=out_logprobs)
-    ptr = _rows_ptr(logits, "logits", types)
-    _check("pld_verify", load().pld_verify(
-        ctx, ptr, types[logits.dtype], int(logits_stride), int(rows),
-        _dev_ptr(draft, "draft", i32), _dev_ptr(draft_len, "draft_len", i32),
-        _dev_ptr(src, "src", torch.int64), _dev_ptr(draft_probs, "draft_probs", f32), int(head),
-        _dev_ptr(temperature, "temperature", f32), _dev_ptr(uniform, "uniform", f32), int(batch),
-        _dev_ptr(out_tokens, "out_tokens", i32), _dev_ptr(out_accepted, "out_accepted", i32),
-        _dev_ptr(out_counts, "out_counts", i32), _dev_ptr(out_logprobs, "out_logprobs", f32),
-        _stream(stream)))
+    ptr = _rows_arg(logits, "logits", types, dev)
+    st = (_lib or load()).pld_verify(
+        ctx, ptr, types[logits.dtype], logits_stride, rows, _arg(draft, "draft", i32, dev),
+        _arg(draft_len, "draft_len", i32, dev), _arg(src, "src", t["i64"], dev),
+        _arg(draft_probs, "draft_probs", f32, dev), head,
+        _arg(temperature, "temperature", f32, dev), _arg(uniform, "uniform", f32, dev), batch,
+        _arg(out_tokens, "out_tokens", i32, dev), _arg(out_accepted, "out_accepted", i32, dev),
+        _arg(out_counts, "out_counts", i32, dev), _arg(out_logprobs, "out_logprobs", f32, dev),
+        _stream(stream))
+    if st:
+        _check("pld_verify", st)
 
 
 def pld_sync(ctx: int, stream=None) -> int:
