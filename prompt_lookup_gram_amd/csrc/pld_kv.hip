@@ -94,6 +94,13 @@ __global__ __launch_bounds__(kThreads) void append_words(KvAppendArgs a, uint32_
         const int32_t pitch = dim + kPad, words = dim / 8;
         const T *v = (const T *)a.v + ((int64_t)b * g.rows - (length - 1)) * a.kv_stride +
                      (int64_t)h * dim;
+        // (a thread stores the same 8 positions of every dim it takes)
+        static_assert(kThreads % (kSpan / 8) == 0, "");
+        const int32_t at = tid % (kSpan / 8) * 8;
+        const int64_t first = p0 + at;
+        const bool any = first + 8 > from && first < to;
+        const bool whole = first >= from && first + 8 <= to;
+        const int32_t page = any ? page_of(g, b, (int32_t)(first > from ? first : from)) : -1;
         for (int32_t i = tid; i < (int32_t)(to - from) * words; i += kThreads) {
             const int64_t p = from + i / words;
             const int32_t d = i % words * 8;
@@ -106,21 +113,16 @@ __global__ __launch_bounds__(kThreads) void append_words(KvAppendArgs a, uint32_
         }
         __syncthreads();
         const float scale = g.v_scale ? g.v_scale[h] : 1.0f;
+        if (page < 0)
+            return;  // (a bad page is reported by the row's K)
         for (int32_t i = tid; i < kSpan / 8 * dim; i += kThreads) {
-            const int32_t d = i / (kSpan / 8), at = i % (kSpan / 8) * 8;
-            const int64_t p = p0 + at;
-            if (p + 8 <= from || p >= to)
-                continue;
-            const int32_t page = page_of(g, b, (int32_t)(p > from ? p : from));
-            if (page < 0)
-                continue;  // (reported by the row's K)
+            const int32_t d = i / (kSpan / 8);
             C *out = (C *)a.v_cache + (((int64_t)page * g.kv_heads + h) * dim + d) * tokens +
-                     (p & (tokens - 1));
-            const bool whole = p >= from && p + 8 <= to;
+                     (first & (tokens - 1));
             float y[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                y[k] = whole || (p + k >= from && p + k < to)
+                y[k] = whole || (first + k >= from && first + k < to)
                            ? to_f32(tile[(at + k) * pitch + d]) / scale
                            : 0.0f;
             if (whole) {
@@ -128,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void append_words(KvAppendArgs a, uint32_
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    if (p + k >= from && p + k < to)
+                    if (first + k >= from && first + k < to)
                         out[k] = from_f32<C>(y[k]);
             }
         }
@@ -147,36 +149,71 @@ __global__ __launch_bounds__(kThreads) void append_words(KvAppendArgs a, uint32_
         return;
     }
     const int32_t live = n - t0 < R ? n - t0 : R;
+    int32_t *pages = (int32_t *)(cs + R * kMaxPairs);
+    // units of a head: with the half layout a word of the first half and its
+    // partner are one, else every word is one
+    const int32_t twos = a.interleaved ? 0 : pairs / 8;
+    const uint32_t units = dim / 8 - twos;
+    const uint32_t q_heads = a.q ? g.q_heads : 0, heads = q_heads + g.kv_heads;
+    const uint32_t all = live * heads * units;
+    struct Unit {
+        Eight<T> u, v;
+        uint32_t unit, h, t;
+    };
+    const auto fetch = [&](uint32_t i) {
+        Unit x;
+        x.unit = i % units;
+        const uint32_t hr = i / units;
+        x.h = hr % heads;
+        x.t = hr / heads;
+        const int64_t r = (int64_t)b * g.rows + t0 + x.t;
+        const T *from = x.h < q_heads ? (const T *)a.q + r * a.q_stride + (int64_t)x.h * dim
+                                      : (const T *)a.k + r * a.kv_stride +
+                                            (int64_t)(x.h - q_heads) * dim;
+        const bool two = x.unit < (uint32_t)twos;
+        const T *p = from + (two ? x.unit : x.unit + twos) * 8;
+        x.u = load8(p);
+        x.v = x.u;
+        if (two)
+            x.v = load8(p + pairs);
+        return x;
+    };
+    // Few rows: the first words are on their way before the angles (13.6 ->
+    // 11.1 us for 64 blocks of 16 rows). Many rows hide that latency in each
+    // other and would only lose wavefronts to the registers (326 -> 338 us for
+    // 65,536 rows).
+    constexpr bool kAhead = R == 1;
+    Unit next{};
+    if (kAhead && (uint32_t)tid < all)
+        next = fetch(tid);
+    if (tid >= kThreads - live) {
+        const int32_t t = tid - (kThreads - live);
+        pages[t] = page_of(g, b, length - 1 + t0 + t);
+        if (pages[t] < 0)
+            atomicOr(g.err, (uint32_t)kErrPage);
+    }
     for (int32_t i = tid; i < live * pairs; i += kThreads) {
         float c, s;
         turn(a.turns[i % pairs], length - 1 + t0 + i / pairs, a.magnitude, c, s);
         cs[i] = float2{c, s};
     }
     __syncthreads();
-    // units of a head: with the half layout a word of the first half and its
-    // partner are one, else every word is one
-    const int32_t twos = a.interleaved ? 0 : pairs / 8;
-    const int32_t units = dim / 8 - twos;
-    const int32_t q_heads = a.q ? g.q_heads : 0, heads = q_heads + g.kv_heads;
-    for (int32_t i = tid; i < live * heads * units; i += kThreads) {
-        const int32_t unit = i % units, hr = i / units, h = hr % heads, t = hr / heads;
-        const int32_t p = length - 1 + t0 + t;
-        const int64_t r = (int64_t)b * g.rows + t0 + t;
-        const bool is_q = h < q_heads;
-        const T *x = is_q ? (const T *)a.q + r * a.q_stride + (int64_t)h * dim
-                          : (const T *)a.k + r * a.kv_stride + (int64_t)(h - q_heads) * dim;
-        const float2 *w = cs + t * pairs;
-        const int32_t d = unit < twos ? unit * 8 : (unit + twos) * 8;
+    for (uint32_t i = tid; i < all; i += kThreads) {
+        const Unit x = kAhead ? next : fetch(i);
+        if (kAhead && i + kThreads < all)
+            next = fetch(i + kThreads);
+        const int64_t r = (int64_t)b * g.rows + t0 + x.t;
+        const float2 *w = cs + x.t * pairs;
+        const bool two = x.unit < (uint32_t)twos;
+        const int32_t d = (two ? x.unit : x.unit + twos) * 8;
         float y[8], z[8];
-        const Eight<T> u = load8(x + d);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            y[k] = to_f32(u.x[k]);
-        if (unit < twos) {
-            const Eight<T> v = load8(x + d + pairs);
+            y[k] = to_f32(x.u.x[k]);
+        if (two) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float e = y[k], f = to_f32(v.x[k]);
+                const float e = y[k], f = to_f32(x.v.x[k]);
                 const float2 m = w[d + k];
                 y[k] = e * m.x - f * m.y;
                 z[k] = e * m.y + f * m.x;
@@ -190,20 +227,18 @@ __global__ __launch_bounds__(kThreads) void append_words(KvAppendArgs a, uint32_
                 y[k + 1] = e * m.y + f * m.x;
             }
         }
-        if (is_q) {
-            T *out = (T *)a.out_q + (r * g.q_heads + h) * dim + d;
+        if (x.h < q_heads) {
+            T *out = (T *)a.out_q + (r * g.q_heads + x.h) * dim + d;
             store8<T>(out, y);
-            if (unit < twos)
+            if (two)
                 store8<T>(out + pairs, z);
             continue;
         }
-        const int32_t page = page_of(g, b, p);
-        if (page < 0) {
-            atomicOr(g.err, (uint32_t)kErrPage);
+        const int32_t page = pages[x.t], h = x.h - q_heads;
+        if (page < 0)
             continue;
-        }
         if (g.k_scale) {
-            const float scale = g.k_scale[h - q_heads];
+            const float scale = g.k_scale[h];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 y[k] /= scale;
@@ -211,9 +246,10 @@ __global__ __launch_bounds__(kThreads) void append_words(KvAppendArgs a, uint32_
             }
         }
         C *out = (C *)a.k_cache +
-                 (((int64_t)page * g.kv_heads + h - q_heads) * tokens + (p & (tokens - 1))) * dim + d;
+                 (((int64_t)page * g.kv_heads + h) * tokens +
+                  ((length - 1 + t0 + (int32_t)x.t) & (tokens - 1))) * dim + d;
         store8<C>(out, y);
-        if (unit < twos)
+        if (two)
             store8<C>(out + pairs, z);
     }
 }
@@ -302,7 +338,7 @@ hipError_t launch_cells(const KvAppendArgs &a, hipStream_t s)
     const int64_t storing = (int64_t)g.batch * g.kv_heads * tiles;
     if (turning + storing > 0x7fffffffLL)
         return hipErrorInvalidConfiguration;
-    const size_t turn_lds = (size_t)R * kMaxPairs * sizeof(float2);
+    const size_t turn_lds = (size_t)R * (kMaxPairs * sizeof(float2) + sizeof(int32_t));
     const size_t tile_lds = (size_t)kSpan * (g.head_dim + kPad) * sizeof(T);
     const size_t lds = turn_lds > tile_lds ? turn_lds : tile_lds;
     const dim3 grid((uint32_t)(turning + storing));
