@@ -421,13 +421,13 @@ __device__ __forceinline__ Outcome outcome_of(const VerifyArgs &a, const Space &
     return o;
 }
 
-// Writes a request's outputs but for the last token, and clears its
-// counters; the whole workgroup.
+// Writes a request's outputs but for the last token, and clears its counters;
+// `threads` threads, this one the `first`.
 __device__ __forceinline__ void finish(const VerifyArgs &a, const Space &sp, int32_t b,
-                                       const Outcome &o)
+                                       const Outcome &o, int32_t first, int32_t threads)
 {
     const int64_t r = (int64_t)b * a.rows;
-    for (int32_t t = threadIdx.x; t < a.rows; t += kThreads) {
+    for (int32_t t = first; t < a.rows; t += threads) {
         sp.arrived[r + t] = 0;
         if (!o.none && t == o.at)
             continue;
@@ -436,7 +436,7 @@ __device__ __forceinline__ void finish(const VerifyArgs &a, const Space &sp, int
         if (a.out_logprobs)
             a.out_logprobs[r + t] = drafted ? sp.rows[r + t].logp : 0.0f;
     }
-    if (threadIdx.x == 0) {
+    if (first == 0) {
         a.out_accepted[b] = o.none ? 0 : o.at;
         a.out_counts[b] = o.none ? 0 : o.at + 1;
         sp.stop[b] = kNever;
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
     const float tf = temperature(a, b);
     if (o.none || tf == 0.0f) {
         if (group == 0) {
-            finish(a, sp, b, o);
+            finish(a, sp, b, o, tid, kThreads);
             if (!o.none && tid == 0)
                 commit(a, b, o, o.row.arg, -log(o.row.total));
         }
@@ -551,48 +551,68 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
     if (!lds_say)
         return;
 
-    // the last workgroup: the unit that holds the goal, then the token
-    finish(a, sp, b, o);
-    if (tid < kWave) {
-        double s = tid < draws ? peek(sums + tid) : 0.0;
-        double all = s;
-        for (int32_t i = tid + kWave; i < draws; i += kWave)
-            all += peek(sums + i);
-        all = wave_sum(all);
+    // the last workgroup: one wavefront finds the unit that holds the goal,
+    // the others write what is known already
+    if (tid >= kWave)
+        finish(a, sp, b, o, tid - kWave, kThreads - kWave);
+    else {
+        // a lane takes `per` units in a row: first whose share holds the goal,
+        // then which of its units
+        const int32_t per = (draws + kWave - 1) / kWave;
+        const auto share = [&] {
+            double s = 0.0;
+#pragma unroll 8
+            for (int32_t i = tid * per; i < (tid + 1) * per; ++i)
+                s += i < draws ? peek(sums + i) : 0.0;
+            return s;
+        };
+        double s = share(), all = wave_sum(s);
         if (EXCESS && !(all > 0.0)) {  // (then it is 0)
             // nothing exceeds q: draw from the weights
             over = nullptr;
             sums = sp.weights + (int64_t)b * draws;
-            s = tid < draws ? peek(sums + tid) : 0.0;
-            all = s;
-            for (int32_t i = tid + kWave; i < draws; i += kWave)
-                all += peek(sums + i);
-            all = wave_sum(all);
+            s = share();
+            all = wave_sum(s);
         }
         const double goal = (double)o.u * all;
-        double before = 0.0, at_before = 0.0;
+        double before = 0.0;
         int32_t at = -1;
-        for (int32_t base = 0; base < draws; base += kWave) {
-            if (base > 0)
-                s = base + tid < draws ? peek(sums + base + tid) : 0.0;
-            double run = s;  // inclusive
+        // the first of 64 shares whose running sum passes the goal (the last
+        // with a weight where rounding left none); `before`: what precedes it
+        const auto find = [&](double v) {
+            double run = v;  // inclusive
             for (int i = 1; i < kWave; i <<= 1) {
                 const double y = __shfl_up(run, i);
                 if (tid >= i)
                     run += y;
             }
-            const unsigned long long over_goal = __ballot(s > 0.0 && before + run > goal);
-            const unsigned long long live = __ballot(s > 0.0);
-            if (live) {
-                // (the last unit with a weight stands in if rounding left none)
-                const int k = over_goal ? __builtin_ctzll(over_goal) : 63 - __builtin_clzll(live);
-                at = base + k;
-                at_before = before + __shfl(run, k) - __shfl(s, k);
+            const uint64_t past = __ballot(v > 0.0 && before + run > goal);
+            const uint64_t live = __ballot(v > 0.0);
+            if (!live)
+                return -1;
+            const int k = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(live);
+            before += __shfl(run, k) - __shfl(v, k);
+            return k;
+        };
+        int32_t from = 0, count = draws;
+        int k = find(s);
+        if (k >= 0) {
+            from = k * per;
+            count = from + per < draws ? per : draws - from;
+            // (more than 64 units a lane: the same again with shares of them)
+            while (count > kWave) {
+                const int32_t step = (count + kWave - 1) / kWave;
+                double v = 0.0;
+                for (int32_t i = tid * step; i < (tid + 1) * step && i < count; ++i)
+                    v += peek(sums + from + i);
+                k = find(v);
+                count = k * step + step < count ? step : count - k * step;
+                from += k * step;
             }
-            before += __shfl(run, kWave - 1);
-            if (over_goal)
-                break;
+            k = find(tid < count ? peek(sums + from + tid) : 0.0);
+            at = from + k;
         }
+        const double at_before = before;
         if (tid == 0) {
             lds_piece = at;
             lds_before = at_before;
