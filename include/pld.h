@@ -665,6 +665,10 @@ pld_status pld_target_params_default(pld_target_params *params);
  * draft calls take it). One context serves every layer of a model in turn;
  * calls that overlap in time need contexts of their own (see the top), and
  * so do captured graphs that may run at the same time.
+ * Memory beyond pld_create's: with heads, partial results of at most 262,144
+ * query rows of head_dim + 2 floats (136 MB at head_dim 128; fewer for contexts
+ * that cannot need them); with a vocab, max_batch * max_rows * vocab / 128 bytes
+ * and a little more.
  *  stream: as in pld_create.
  * Errors: PLD_EINVAL (null, a field outside its range), PLD_ENOMEM, PLD_EHIP.
  */

@@ -582,11 +582,12 @@ def pld_kv_append(ctx: int, q, q_stride: int, k, v, kv_stride: int, rows: int, l
     t = _types or _verify_types()
     dev, i32, half, cells, f32 = _device(t), t["i32"], t["half"], t["cells"], t["f32"]
     st = (_lib or load()).pld_kv_append(
-        ctx, _rows_arg(q, "q", half, dev), q_stride, _rows_arg(k, "k", half, dev),
-        _rows_arg(v, "v", half, dev), kv_stride, rows, _arg(lengths, "lengths", i32, dev),
-        _arg(draft_len, "draft_len", i32, dev), batch, _arg(page_table, "page_table", i32, dev),
-        table_stride, _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev),
-        n_pages, _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev),
+        ctx, _rows_arg(q, "q", half, dev), int(q_stride), _rows_arg(k, "k", half, dev),
+        _rows_arg(v, "v", half, dev), int(kv_stride), int(rows),
+        _arg(lengths, "lengths", i32, dev), _arg(draft_len, "draft_len", i32, dev), int(batch),
+        _arg(page_table, "page_table", i32, dev), int(table_stride),
+        _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev),
+        int(n_pages), _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev),
         _arg(out_q, "out_q", half, dev), _stream(stream))
     if st:
         _check("pld_kv_append", st)
@@ -600,12 +601,13 @@ def pld_attend(ctx: int, q, q_stride: int, rows: int, lengths, draft_len, max_le
     t = _types or _verify_types()
     dev, i32, half, cells, f32 = _device(t), t["i32"], t["half"], t["cells"], t["f32"]
     st = (_lib or load()).pld_attend(
-        ctx, _rows_arg(q, "q", half, dev), q_stride, rows, _arg(lengths, "lengths", i32, dev),
-        _arg(draft_len, "draft_len", i32, dev), max_len, batch,
-        _arg(page_table, "page_table", i32, dev), table_stride,
-        _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev), n_pages,
-        _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev), scale, window,
-        _arg(out, "out", half, dev), _arg(out_lse, "out_lse", f32, dev), _stream(stream))
+        ctx, _rows_arg(q, "q", half, dev), int(q_stride), int(rows),
+        _arg(lengths, "lengths", i32, dev), _arg(draft_len, "draft_len", i32, dev),
+        int(max_len), int(batch),
+        _arg(page_table, "page_table", i32, dev), int(table_stride),
+        _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev), int(n_pages),
+        _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev), float(scale),
+        int(window), _arg(out, "out", half, dev), _arg(out_lse, "out_lse", f32, dev), _stream(stream))
     if st:
         _check("pld_attend", st)
 
@@ -623,10 +625,11 @@ def pld_verify(ctx: int, logits, logits_stride: int, rows: int, draft, draft_len
         raise TypeError("logits: expected a torch tensor")
     ptr = _rows_arg(logits, "logits", types, dev)
     st = (_lib or load()).pld_verify(
-        ctx, ptr, types[logits.dtype], logits_stride, rows, _arg(draft, "draft", i32, dev),
+        ctx, ptr, types[logits.dtype], int(logits_stride), int(rows),
+        _arg(draft, "draft", i32, dev),
         _arg(draft_len, "draft_len", i32, dev), _arg(src, "src", t["i64"], dev),
-        _arg(draft_probs, "draft_probs", f32, dev), head,
-        _arg(temperature, "temperature", f32, dev), _arg(uniform, "uniform", f32, dev), batch,
+        _arg(draft_probs, "draft_probs", f32, dev), int(head),
+        _arg(temperature, "temperature", f32, dev), _arg(uniform, "uniform", f32, dev), int(batch),
         _arg(out_tokens, "out_tokens", i32, dev), _arg(out_accepted, "out_accepted", i32, dev),
         _arg(out_counts, "out_counts", i32, dev), _arg(out_logprobs, "out_logprobs", f32, dev),
         _stream(stream))

@@ -207,6 +207,9 @@ __device__ __forceinline__ double sum_again(const T *z, int32_t vocab, float m, 
 }
 
 // One workgroup per piece of a row, W 16-byte words a thread.
+// Measured: 64 requests of up to 16 draft tokens, 151,936 bf16 logits a row:
+// 37 us, 125 MB read where 62 are up to the refusals; one request of 17 rows of
+// 32,000: 7.7 us, the chain of its round trips.
 // (8 wavefronts a SIMD: the rare second sum must not cost the first its
 // registers)
 template <typename T, int W>
@@ -221,6 +224,9 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Space 
     const int32_t b = order % (uint32_t)a.batch, t = order / (uint32_t)a.batch;
     const int wave = tid / kWave, lane = tid % kWave;
     const int32_t d = a.draft_len[b];
+    // (Wavefronts may see `stop` change between them, and some go on without
+    // the others: what they leave is a row behind a refusal, which nothing
+    // looks at and whose verdict cannot lower `stop`.)
     if (t > d || d >= a.rows || peek(sp.stop + b) < t)
         return;
     const T *z = (const T *)a.logits + ((int64_t)b * a.rows + t) * a.stride;
@@ -471,7 +477,9 @@ __device__ __forceinline__ double weight_of(float z, int32_t i, double top, doub
 // kWaves units a workgroup. EXCESS 0: sums of the weights; the last workgroup
 // of a request without q at that row draws. EXCESS 1 (a second launch, when
 // there are drafter probabilities): sums of the excess over q, whose total of
-// the weights the first launch left.
+// the weights the first launch left. Measured: 31 us for 64 rows of 151,936
+// logits (12 of them the 64-bit exponentials, 9.7 million), 12 us for one of
+// 32,000.
 template <typename T, int EXCESS, int E>
 __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, int32_t groups)
 {
