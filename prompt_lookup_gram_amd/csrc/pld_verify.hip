@@ -485,7 +485,7 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
 {
     constexpr int N = 16 / sizeof(T), kUnit = E * kWave, kPer = kUnit / kThreads;
     __shared__ double lds_d[kWaves];
-    __shared__ int32_t lds_say, lds_piece, lds_pick, lds_last;
+    __shared__ int32_t lds_final, lds_over, lds_piece, lds_pick, lds_last;
     __shared__ double lds_before, lds_goal;
     const int32_t b = blockIdx.x / (uint32_t)groups, group = blockIdx.x % (uint32_t)groups;
     const int32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
@@ -554,9 +554,10 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
     if (!EXCESS && q)
         return;
     if (tid == 0)
-        lds_say = arrive(sp.drawn + b) == groups - 1;
+        lds_final = arrive(sp.drawn + b) == groups - 1;
     __syncthreads();
-    if (!lds_say)
+    // (nothing below writes this word: other wavefronts may read it late)
+    if (!lds_final)
         return;
 
     // the last workgroup: one wavefront finds the unit that holds the goal,
@@ -627,11 +628,11 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyArgs a, Space sp, 
             lds_goal = goal;
             lds_pick = 0x7fffffff;
             lds_last = -1;
-            lds_say = over != nullptr;
+            lds_over = over != nullptr;
         }
     }
     __syncthreads();
-    over = lds_say ? q : nullptr;
+    over = lds_over ? q : nullptr;
     const int32_t from = lds_piece * kUnit + tid * kPer;
     double w[kPer], run = 0.0;
     float y[kPer];

@@ -1,0 +1,104 @@
+"""pld_verify's kernels on the host, against the 64-bit reference, over orders
+in which the wavefronts of a workgroup may run (no GPU needed): results, the
+counters left for the next call, and barriers that all of a workgroup reach.
+The tolerance of log probabilities is test_verify_gpu.py's."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import host_verify as H
+import target_reference as R
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    return H.build(tmp_path_factory.mktemp("host"))
+
+
+class Case:
+    def __init__(self, batch, rows, vocab, dtype=H.F32, seed=0, temperature=1.0, head=0, accept=0.7,
+                 dlen=None, zero_excess=False):
+        rng = np.random.default_rng([9501, seed])
+        d = rows - 1
+        z = rng.standard_normal((batch, rows, vocab)) * 2.0
+        self.draft = rng.integers(0, vocab, (batch, max(1, d))).astype(np.int32)[:, :d]
+        self.temp = np.broadcast_to(np.asarray(temperature, np.float32), (batch,)).copy()
+        for b in range(batch):
+            for t in range(d):
+                x, scale = self.draft[b, t], self.temp[b] or 1.0
+                w = np.exp(z[b, t] / scale)
+                if vocab > 1:
+                    z[b, t, x] = scale * np.log((w.sum() - w[x]) * accept / (1 - accept))
+        self.logits, self.z = H.bits(z, dtype)
+        self.dtype, self.rows, self.batch, self.vocab = dtype, rows, batch, vocab
+        self.dlen = np.full(batch, d) if dlen is None else np.asarray(dlen)
+        self.uniform = rng.random((batch, rows)).astype(np.float32)
+        self.probs = None
+        if head:
+            p = np.exp(self.z[:, :head] - self.z[:, :head].max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            # (twice p: nothing exceeds it, the draw falls back to p)
+            q = 2.0 * p if zero_excess else p * np.exp(0.5 * rng.standard_normal(p.shape))
+            if zero_excess:
+                self.uniform[:, :d] = 0.9
+            else:
+                q /= q.sum(-1, keepdims=True)
+            self.probs = q.astype(np.float32)
+
+    def run(self, ctx, **kw):
+        return ctx.verify(self.logits, self.dtype, self.draft, self.dlen, self.uniform,
+                          probs=self.probs, temperature=self.temp, **kw)
+
+    def compare(self, got):
+        tok, acc, cnt, logp = got[:4]
+        for b in range(self.batch):
+            d = int(self.dlen[b])
+            if d < 0:
+                assert (tok[b] == -1).all() and cnt[b] == 0
+                continue
+            head = 0 if self.probs is None else self.probs.shape[1]
+            want, lp = R.verify_one(self.z[b], self.draft[b], d, [t < head for t in range(d)],
+                                    None if self.probs is None else
+                                    self.probs[b].astype(np.float64), float(self.temp[b]),
+                                    self.uniform[b], self.uniform[b, -1])
+            n = len(want)
+            assert cnt[b] == n and acc[b] == n - 1, (b, cnt[b], n)
+            assert tok[b].tolist() == want + [-1] * (self.rows - n), b
+            assert (np.abs(logp[b, :n] - lp) <= 2.0**-17 + 2.0**-23 * np.abs(lp)).all()
+            assert (logp[b, n:] == 0).all()
+
+
+def check(lib, case):
+    ctx = H.Context(lib, case.batch, case.rows, case.vocab)
+    for order in H.ORDERS:
+        got = case.run(ctx, order=order)
+        case.compare(got)
+        assert got[4] == 0
+        assert ctx.clear(), order
+
+
+@pytest.mark.parametrize("dtype", [H.F32, H.F16, H.BF16])
+@pytest.mark.parametrize("vocab", [1, 700, 2049, 9000])
+def test_point_masses(lib, dtype, vocab):
+    check(lib, Case(3, 5, vocab, dtype=dtype, seed=vocab))
+
+
+@pytest.mark.parametrize("head", [1, 3])
+def test_drafter_probabilities(lib, head):
+    check(lib, Case(4, 4, 3001, head=head, temperature=0.7, seed=head))
+
+
+def test_zero_excess_draws_from_p(lib):
+    c = Case(3, 3, 2500, head=2, zero_excess=True, seed=5)
+    check(lib, c)
+
+
+def test_greedy_idle_and_ragged_requests(lib):
+    check(lib, Case(6, 5, 1200, temperature=[0.0, 1.0, 0.0, 0.5, 1.0, 2.0],
+                    dlen=[4, 4, 0, -1, 2, 0], seed=6))
+
+
+def test_more_rows_than_a_wavefront(lib):
+    check(lib, Case(2, 70, 130, accept=0.95, seed=7))
