@@ -218,16 +218,19 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(VerifyArgs a, Space 
     constexpr int N = 16 / sizeof(T);
     constexpr int kPiece = W * N * kThreads;
     __shared__ float lds_max[kWaves], lds_sum[kWaves];
-    __shared__ int32_t lds_arg[kWaves];
+    __shared__ int32_t lds_arg[kWaves], lds_stop;
     const int32_t piece = blockIdx.x % pieces, tid = threadIdx.x;
     const uint32_t order = blockIdx.x / pieces;
     const int32_t b = order % (uint32_t)a.batch, t = order / (uint32_t)a.batch;
     const int wave = tid / kWave, lane = tid % kWave;
     const int32_t d = a.draft_len[b];
-    // (Wavefronts may see `stop` change between them, and some go on without
-    // the others: what they leave is a row behind a refusal, which nothing
-    // looks at and whose verdict cannot lower `stop`.)
-    if (t > d || d >= a.rows || peek(sp.stop + b) < t)
+    if (t > d || d >= a.rows)
+        return;
+    // (`stop` may change between two reads: one decides for all wavefronts)
+    if (tid == 0)
+        lds_stop = peek(sp.stop + b);
+    __syncthreads();
+    if (lds_stop < t)
         return;
     const T *z = (const T *)a.logits + ((int64_t)b * a.rows + t) * a.stride;
     const float tf = temperature(a, b);

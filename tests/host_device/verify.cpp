@@ -27,9 +27,9 @@ int host_counters_clear(void *ws, int32_t batch, int32_t rows, int32_t vocab)
     return 1;
 }
 
-// order: the wavefronts' order, `waves` of them. refuse_row > 0: from the
-// second wavefront of any workgroup on, whoever looks at `stop` for the first
-// time finds that row refused meanwhile (by another workgroup).
+// order: the wavefronts' order, `waves` of them. refuse_row > 0: `refuse_row`
+// is refused by another workgroup between the looks that two wavefronts of a
+// workgroup take at `stop`: the first finds no refusal, the others find it.
 // report: broken barriers, stuck workgroups.
 int host_verify(const pld::VerifyArgs *a, const int32_t *order, int32_t waves, int32_t refuse_row,
                 int64_t *report)
@@ -40,12 +40,17 @@ int host_verify(const pld::VerifyArgs *a, const int32_t *order, int32_t waves, i
     s.on_load = nullptr;
     const pld::Space sp = pld::space_of((char *)a->stats, a->max_batch, a->max_rows, a->vocab,
                                         nullptr);
+    uint32_t looked_block = ~0u, looked_wave = 0;
     if (refuse_row > 0)
-        s.on_load = [=](const void *p) {
+        s.on_load = [&](const void *p) {
             int32_t *word = (int32_t *)p;
-            if (word >= sp.stop && word < sp.stop + a->max_batch && threadIdx.x >= 64 &&
-                *word > refuse_row)
-                *word = refuse_row;
+            if (word < sp.stop || word >= sp.stop + a->max_batch)
+                return;
+            if (looked_block != blockIdx.x) {
+                looked_block = blockIdx.x;
+                looked_wave = threadIdx.x / 64;
+            }
+            *word = threadIdx.x / 64 == looked_wave ? pld::kNever : refuse_row;
         };
     const hipError_t e = pld::launch_verify(*a, nullptr);
     s.on_load = nullptr;

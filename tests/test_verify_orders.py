@@ -102,3 +102,16 @@ def test_greedy_idle_and_ragged_requests(lib):
 
 def test_more_rows_than_a_wavefront(lib):
     check(lib, Case(2, 70, 130, accept=0.95, seed=7))
+
+
+def test_a_refusal_seen_by_part_of_a_workgroup(lib):
+    """A row is refused while the wavefronts of a workgroup behind it start:
+    all of them go on or none does, and the results are the same."""
+    c = Case(2, 6, 5000, seed=8, accept=0.9)
+    c.uniform[:, 1] = 1.0 - 2.0**-24      # refused at position 1 at the latest
+    ctx = H.Context(lib, c.batch, c.rows, c.vocab)
+    for order in H.ORDERS:
+        got = c.run(ctx, order=order, refuse_row=1)
+        c.compare(got)
+        assert ctx.clear()
+        assert got[5] == 0, f"{got[5]} barriers that part of a workgroup never reached"
