@@ -277,6 +277,7 @@ def pld_scan_tile(ctx: int, batch: int) -> int:
 
 def pld_destroy(ctx: int) -> None:
     _check("pld_destroy", load().pld_destroy(ctx))
+    _target_types.pop(ctx, None)
 
 
 def pld_configure(ctx: int, tile_tokens: int = 0, fused_gather: int = -1) -> None:
@@ -502,6 +503,8 @@ def pld_append_draft_ngram(ctx: int, tokens, tokens_stride: int, counts, batch: 
 # The verify step's calls take many tensors and are small: their checks are
 # one pass over each tensor, with the dtypes looked up once.
 _types = None
+# (dtype, cache_dtype) of the live target contexts that pld_create_target made
+_target_types = {}
 
 
 def _verify_types():
@@ -509,9 +512,12 @@ def _verify_types():
     if _types is None:
         import torch
         half = (torch.float16, torch.bfloat16)
+        of = {PLD_F16: torch.float16, PLD_BF16: torch.bfloat16, PLD_E4M3: torch.float8_e4m3fn}
         _types = {"tensor": torch.Tensor, "i32": (torch.int32,),
                   "i64": (torch.int64,), "f32": (torch.float32,), "half": half,
                   "cells": half + (torch.float8_e4m3fn,),
+                  # a context's types: those of its q, k, v and outputs, of its cache
+                  "of": {(x, y): ((of[x],), (of[y],)) for x in (PLD_F16, PLD_BF16) for y in of},
                   "logits": {torch.float32: PLD_F32, torch.float16: PLD_F16,
                              torch.bfloat16: PLD_BF16},
                   "device": torch.cuda.current_device, "gpu": torch.cuda.is_available()}
@@ -566,11 +572,20 @@ def pld_target_params_default() -> PldTargetParams:
 
 
 def pld_create_target(params: PldTargetParams, stream=None) -> int:
-    """A context for the verify step's calls (include/pld.h)."""
+    """A context for the verify step's calls (include/pld.h). They refuse
+    tensors of other types than its dtype and cache_dtype."""
     ctx = ctypes.c_void_p()
     _check("pld_create_target", load().pld_create_target(
         ctypes.byref(ctx), ctypes.byref(params), _create_stream(stream)))
+    if params.q_heads > 0:
+        _target_types[ctx.value] = (params.dtype, params.cache_dtype)
     return ctx.value
+
+
+def _target_dtypes(t, ctx: int):
+    """The dtypes a context takes: of q, k, v and outputs, and of its cache
+    (any of the calls' where the context was not made here)."""
+    return t["of"].get(_target_types.get(ctx)) or (t["half"], t["cells"])
 
 
 def pld_kv_append(ctx: int, q, q_stride: int, k, v, kv_stride: int, rows: int, lengths,
@@ -580,7 +595,8 @@ def pld_kv_append(ctx: int, q, q_stride: int, k, v, kv_stride: int, rows: int, l
     cache (include/pld.h). q, k and v may be slices whose rows lie q_stride
     and kv_stride elements apart."""
     t = _types or _verify_types()
-    dev, i32, half, cells, f32 = _device(t), t["i32"], t["half"], t["cells"], t["f32"]
+    dev, i32, f32 = _device(t), t["i32"], t["f32"]
+    half, cells = _target_dtypes(t, ctx)
     st = (_lib or load()).pld_kv_append(
         ctx, _rows_arg(q, "q", half, dev), int(q_stride), _rows_arg(k, "k", half, dev),
         _rows_arg(v, "v", half, dev), int(kv_stride), int(rows),
@@ -599,7 +615,8 @@ def pld_attend(ctx: int, q, q_stride: int, rows: int, lengths, draft_len, max_le
                out_lse=None, stream=None) -> None:
     """Attention of the block's rows over the paged cache (include/pld.h)."""
     t = _types or _verify_types()
-    dev, i32, half, cells, f32 = _device(t), t["i32"], t["half"], t["cells"], t["f32"]
+    dev, i32, f32 = _device(t), t["i32"], t["f32"]
+    half, cells = _target_dtypes(t, ctx)
     st = (_lib or load()).pld_attend(
         ctx, _rows_arg(q, "q", half, dev), int(q_stride), int(rows),
         _arg(lengths, "lengths", i32, dev), _arg(draft_len, "draft_len", i32, dev),

@@ -96,6 +96,62 @@ def test_binding_checks_tensors_before_the_call():
         B.pld_verify(1, 1234, 8, 1, None, None, None, None, 0, None, None, 0, None, None, None)
 
 
+class _Recorder:
+    """Stands for the library: takes every call."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            if name == "pld_create_target":
+                args[0]._obj.value = 4096
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("dt,cache", [("bfloat16", "bfloat16"), ("float16", "float16"),
+                                      ("bfloat16", "float8_e4m3fn"), ("float16", "float8_e4m3fn")])
+def test_binding_checks_dtypes_against_the_context(monkeypatch, dt, cache):
+    """A cache or rows of another type than the context's would be read and
+    written past their end, or as other numbers: refused before the call."""
+    import torch
+    lib = _Recorder()
+    monkeypatch.setattr(B, "_lib", lib)
+    # CPU tensors pass for the device's: their get_device() is -1
+    monkeypatch.setattr(B, "_types", {**B._verify_types(), "gpu": True, "device": lambda: -1})
+    types = {"float16", "bfloat16", "float8_e4m3fn"}
+    p = params(dtype=B.PLD_TYPES[getattr(torch, dt)],
+               cache_dtype=B.PLD_TYPES[getattr(torch, cache)])
+    ctx = B.pld_create_target(p, 0)
+    one = torch.ones(4, dtype=torch.int32)
+
+    def tensor(name):
+        return torch.zeros(64, dtype=getattr(torch, name))
+
+    def attend(q, k, v, out):
+        B.pld_attend(ctx, tensor(q), 64, 1, one, one, 0, 1, one, 1, tensor(k), tensor(v), 1,
+                     out=tensor(out), stream=0)
+
+    def append(q, k, v, kc, vc, out):
+        B.pld_kv_append(ctx, tensor(q), 64, tensor(k), tensor(v), 64, 1, one, one, 1, one, 1,
+                        tensor(kc), tensor(vc), 1, out_q=tensor(out), stream=0)
+    for call, good in ((attend, (dt, cache, cache, dt)), (append, (dt, dt, dt, cache, cache, dt))):
+        lib.calls.clear()
+        call(*good)
+        assert len(lib.calls) == 1
+        for i, right in enumerate(good):
+            for wrong in types - {right}:
+                with pytest.raises(ValueError):
+                    call(*good[:i], wrong, *good[i + 1:])
+        assert len(lib.calls) == 1, "a call with another type reached the library"
+    # the handle of a context that is gone says nothing about the next one's types
+    B.pld_destroy(ctx)
+    attend("bfloat16", "bfloat16", "bfloat16", "bfloat16")
+    attend("float16", "float8_e4m3fn", "float8_e4m3fn", "float16")
+
+
 # ---------------------------------------------------------------------------
 # the reference, against values derived by hand
 # ---------------------------------------------------------------------------
