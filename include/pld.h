@@ -667,8 +667,11 @@ pld_status pld_target_params_default(pld_target_params *params);
  * so do captured graphs that may run at the same time.
  * Memory beyond pld_create's: with heads, partial results of at most 262,144
  * query rows of head_dim + 2 floats (136 MB at head_dim 128; fewer for contexts
- * that cannot need them); with a vocab, max_batch * max_rows * vocab / 128 bytes
- * and a little more.
+ * that cannot need them); with a vocab, at most
+ * max_batch * vocab * (max_rows / 128 + 1 / 32) bytes, plus 52 bytes a row and
+ * 24 a request. max_rows counts in it for blocks of prompts too: a context that
+ * takes long prompts into the cache is better made without a vocab, beside
+ * one without heads for pld_verify.
  *  stream: as in pld_create.
  * Errors: PLD_EINVAL (null, a field outside its range), PLD_ENOMEM, PLD_EHIP.
  */

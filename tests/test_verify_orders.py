@@ -5,6 +5,9 @@ The tolerance of log probabilities is test_verify_gpu.py's."""
 
 from __future__ import annotations
 
+import os
+import re
+
 import numpy as np
 import pytest
 
@@ -115,3 +118,20 @@ def test_a_refusal_seen_by_part_of_a_workgroup(lib):
         c.compare(got)
         assert ctx.clear()
         assert got[5] == 0, f"{got[5]} barriers that part of a workgroup never reached"
+
+
+def test_workspace_is_what_the_header_says(lib):
+    with open(os.path.join(H.ROOT, "include", "pld.h")) as f:
+        text = " ".join(line.strip().removeprefix("* ") for line in f)
+    m = re.search(r"max_batch \* vocab \* \(max_rows / (\d+) \+ 1 / (\d+)\) bytes, plus (\d+) "
+                  r"bytes a row and (\d+) a request", text)
+    assert m, "the header states no bound"
+    per_row, once, row, request = (int(x) for x in m.groups())
+    for batch in (1, 3, 64):
+        for rows in (1, 2, 17, 500):
+            for vocab in (1, 511, 2048, 32000, 151936, 1 << 24):
+                says = batch * (vocab * (rows / per_row + 1 / once) + rows * row + request)
+                size = lib.host_workspace(batch, rows, vocab)
+                assert size <= says, (batch, rows, vocab)
+                if vocab >= 32000:
+                    assert size > 0.97 * says
