@@ -132,6 +132,5 @@ def test_workspace_is_what_the_header_says(lib):
             for vocab in (1, 511, 2048, 32000, 151936, 1 << 24):
                 says = batch * (vocab * (rows / per_row + 1 / once) + rows * row + request)
                 size = lib.host_workspace(batch, rows, vocab)
-                assert size <= says, (batch, rows, vocab)
-                if vocab >= 32000:
-                    assert size > 0.97 * says
+                # (the last piece of a row, and of a request's sums, is 16 bytes)
+                assert 0 <= says - size <= 16 * batch * (rows + 1), (batch, rows, vocab)
