@@ -134,3 +134,42 @@ def test_workspace_is_what_the_header_says(lib):
                 size = lib.host_workspace(batch, rows, vocab)
                 # (the last piece of a row, and of a request's sums, is 16 bytes)
                 assert 0 <= says - size <= 16 * batch * (rows + 1), (batch, rows, vocab)
+
+
+@pytest.mark.parametrize("dtype", [H.F32, H.F16, H.BF16])
+@pytest.mark.parametrize("head", [0, 1])
+def test_full_batches(lib, dtype, head):
+    """8,192 logits a piece and units of 2,048 to draw from: both draw
+    launches, pieces and units that end inside a row of odd length."""
+    c = Case(64, 4, 33001, dtype=dtype, head=head, accept=0.5, seed=20 + head,
+             dlen=[3, 2, 1, 0] * 16)
+    ctx = H.Context(lib, c.batch, c.rows, c.vocab)
+    for order in H.ORDERS[:2]:
+        got = c.run(ctx, order=order)
+        c.compare(got)
+        assert got[4] == 0 and ctx.clear()
+
+
+def test_more_units_than_two_steps_of_a_wavefront_find(lib):
+    """Above 64 * 64 units of 2,048 logits a lane's share of the units is
+    itself searched in shares."""
+    vocab = 64 * 64 * 2048 + 12345
+    rng = np.random.default_rng(9502)
+    z = rng.standard_normal((2, 1, vocab), dtype=np.float32)
+    logits, z64 = H.bits(z, H.F16)
+    u = np.array([[0.31], [1 - 2.0**-24]], np.float32)
+    ctx = H.Context(lib, 2, 1, vocab)
+    tok, acc, cnt, logp, err, _ = ctx.verify(logits, H.F16, np.zeros((2, 0)), [0] * 2, u)
+    assert err == 0 and ctx.clear() and (acc == 0).all() and (cnt == 1).all()
+    for b in range(2):
+        p = np.exp(z64[b, 0] - z64[b, 0].max())
+        c = np.cumsum(p)
+        want = int(np.searchsorted(c, float(u[b, 0]) * c[-1], side="right"))
+        # (sums in another order: 64-bit rounding over 8.4 million terms)
+        slack = 2.0**-52 * vocab * c[-1]
+        near = c[want] - float(u[b, 0]) * c[-1] > slack and (
+            want == 0 or float(u[b, 0]) * c[-1] - c[want - 1] > slack)
+        assert not near or tok[b, 0] == want, b
+        assert abs(int(tok[b, 0]) - want) <= 1
+        assert abs(logp[b, 0] - (z64[b, 0, tok[b, 0]] - z64[b, 0].max() - np.log(c[-1]))) <= (
+            2.0**-17 + 2.0**-23 * 20)
