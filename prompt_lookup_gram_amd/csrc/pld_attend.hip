@@ -91,6 +91,14 @@ __device__ __forceinline__ U4 widen8(uint32_t a, uint32_t b)
               Frag<T>::template widen<false>(b), Frag<T>::template widen<true>(b)};
 }
 
+// The factor on the scores. Never 0, where a product of small scales would
+// be: 0 times a masked score's -infinity is NaN.
+__device__ __forceinline__ float factor(float c)
+{
+    const float x = fabsf(c);
+    return x < FLT_MIN ? FLT_MIN : x;
+}
+
 // How a launch splits the positions: spans of `span` positions (a multiple
 // of the tile), `splits` of them at most; partial results of a request whose
 // positions take more than one.
@@ -551,7 +559,7 @@ struct Narrow : Tiles<T, C, D, MB> {
         // the query rows as operands
         const float ks = g.k_scale ? g.k_scale[w.h] : 1.0f;
         const float c0 = a.scale * ks * kLog2e;
-        const float c = fabsf(c0);
+        const float c = factor(c0);
         const uint32_t flip = c0 < 0.0f ? 0x80008000u : 0u;
         U4 *qf = (U4 *)lds;
         U4 q1[MB == 1 ? KS : 1];
@@ -760,7 +768,7 @@ struct Wide : Tiles<T, C, D, RB> {
 
         const float ks = g.k_scale ? g.k_scale[w.h] : 1.0f;
         const float c0 = a.scale * ks * kLog2e;
-        const float c = fabsf(c0);
+        const float c = factor(c0);
         const uint32_t flip = c0 < 0.0f ? 0x80008000u : 0u;
         U4 q[RB][KS];
         int32_t pos[RB], low[RB];
