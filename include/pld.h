@@ -744,7 +744,9 @@ pld_status pld_kv_append(pld_ctx *ctx, const void *q, int64_t q_stride, const vo
  *            NaN and sets the sticky flag (PLD_ECAPACITY).
  *  scale:    0 means 1 / sqrt(head_dim).
  *  window:   >= 0.
- *  out:      device dtype [batch * rows][q_heads * head_dim], dense.
+ *  out:      device dtype [batch * rows][q_heads * head_dim], dense. It may be q
+ *            itself when q_stride is q_heads * head_dim, and overlaps no input
+ *            otherwise.
  *  out_lse:  device float [batch * rows][q_heads] or NULL.
  * A row that sees a bad page is written as NaN (other rows of its request may
  * be, too). Results do not depend on timing.

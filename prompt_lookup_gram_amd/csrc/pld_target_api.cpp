@@ -339,6 +339,9 @@ pld_status pld_attend(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t row
                     "(got %lld)", (long long)q_stride);
     if (((uintptr_t)q | (uintptr_t)out) & 15u)
         return fail(PLD_EINVAL, "q and out must be 16-byte aligned");
+    if (q && q == out && q_stride != (int64_t)p.q_heads * p.head_dim)
+        return fail(PLD_EINVAL, "out in q's place needs q_stride %lld",
+                    (long long)p.q_heads * p.head_dim);
     if ((uintptr_t)out_lse & 3u)
         return fail(PLD_EINVAL, "out_lse must be 4-byte aligned");
     if (!isfinite(scale))

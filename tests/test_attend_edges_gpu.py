@@ -1,9 +1,9 @@
 """pld_attend (HIP, gfx950) at the edges of its arguments: scales so small
-that they vanish in 32 bits. Tolerances are test_attend_gpu.py's."""
+that they vanish in 32 bits, and results in q's place. Tolerances are
+test_attend_gpu.py's."""
 
 from __future__ import annotations
 
-import numpy as np
 import pytest
 
 from prompt_lookup_gram_amd import binding as B
@@ -19,3 +19,42 @@ def test_scales_that_vanish_weigh_every_position_the_same(cache, scale, rows):
     # (1e-45 times a cell scale below 1 is 0; masked scores stay out all the same)
     check([70, 33, 300], [rows - 1, 0, rows // 2], rows, scale=scale, cache=cache, window=40,
           seed=20)
+
+
+@pytest.mark.parametrize("rows,lengths", [(1, [70, 9000]), (4, [300, 20]), (8, [9000, 5]),
+                                          (40, [700, 3])])
+def test_out_in_the_place_of_q(rows, lengths):
+    import torch
+    c = Case(lengths, [rows - 1, rows // 2], rows, hq=8, hk=2, dim=128, page=64, seed=21)
+    ctx = c.context()
+    try:
+        out, lse = c.outputs()
+        c.call(ctx, out, lse)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        c.compare(out, lse)
+        q, again = c.q, torch.empty_like(lse).fill_(7.0)
+        c.q = q.clone()
+        c.call(ctx, c.q, again)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        got = c.q.view(out.shape)
+        for i in range(2):
+            n = c.dlen[i] + 1
+            assert torch.equal(got[i, :n], out[i, :n]) and torch.equal(again[i, :n], lse[i, :n])
+            # rows past the block are left as they were
+            assert torch.equal(got[i, n:], q.view(out.shape)[i, n:])
+    finally:
+        B.pld_destroy(ctx)
+
+
+def test_out_over_strided_q_is_refused():
+    import torch
+    c = Case([50, 20], [2, 1], 3, pad=24, seed=22)
+    ctx = c.context()
+    try:
+        kept = c.q.clone()
+        with pytest.raises(B.PldError, match="q_stride") as e:
+            c.call(ctx, c.q, None)
+        assert e.value.status == B.PLD_EINVAL
+        assert B.pld_sync(ctx) == B.PLD_OK and torch.equal(c.q, kept)
+    finally:
+        B.pld_destroy(ctx)
