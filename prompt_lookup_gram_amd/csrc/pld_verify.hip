@@ -78,6 +78,7 @@ struct Space {
 };
 
 constexpr int kMinPiece = 2048;
+constexpr int64_t kManyPieces = 32;
 
 __host__ __device__ int64_t pieces_of(int32_t vocab, int piece)
 {
@@ -713,14 +714,24 @@ template <typename T>
 hipError_t launch_typed(const VerifyArgs &a, hipStream_t s)
 {
     const Space sp = space_of((char *)a.stats, a.max_batch, a.max_rows, a.vocab, nullptr);
-    // 8,192 logits a piece, or 2,048 while that leaves the chip half empty
+    // 8,192 logits a piece from kManyPieces of them on, else 2,048. A few pieces
+    // leave the chip empty, and the short ones are read sooner (the call, one row
+    // of 32,000: 16.8 us short, 17.4 long). Many short ones cost more to count in
+    // and to join than they spread: 20 long pieces 18.2 us both ways, 76 of them
+    // 21.5 short and 19.2 long, 304 29.8 and 21.6, 4,864 57.8 and 43.7. A row that
+    // one short piece holds takes it at any number (64 x 16 rows of 1,500: 18.4
+    // and 19.5).
     constexpr int kWide = 8192 / (16 / sizeof(T)) / kThreads;
     const int64_t rows = (int64_t)a.batch * a.rows, wide = pieces_of(a.vocab, 8192);
-    hipError_t e = wide * rows >= 512
+    hipError_t e = wide * rows >= kManyPieces && a.vocab > kMinPiece
                        ? start(stats_kernel<T, kWide>, kThreads, a, sp, rows, wide, s)
                        : start(stats_kernel<T, kWide / 4>, kThreads, a, sp, rows,
                                pieces_of(a.vocab, kMinPiece), s);
-    // units of 2,048 logits to draw from, or of 512 while they are few
+    // units of 2,048 logits to draw from, or of 512 while they are few and a
+    // unit's exponentials are what is waited for (the call, two rows a request:
+    // 0.14 million logits 19.5 us with 512, 24.7 with 2,048; 1.2 million 37.5 and
+    // 37.9; 1.6 million 31.7 and 31.2; 2.4 million 35.1 and 30.2; 9.7 million 72.5
+    // and 45.0)
     if (e == hipSuccess)
         e = (int64_t)a.batch * a.vocab >= (2 << 20) ? launch_draw<T, 32>(a, sp, s)
                                                      : launch_draw<T, 8>(a, sp, s);

@@ -60,9 +60,18 @@ def test_both_sides_of_the_draws_unit(vocab, head):
 @pytest.mark.parametrize("batch,rows", [(73, 7), (64, 8), (57, 9)])
 @pytest.mark.parametrize("vocab", [8192, 8191])
 @pytest.mark.parametrize("dt", ["f32", "f16"])
-def test_both_sides_of_the_statistics_piece(batch, rows, vocab, dt):
+def test_many_pieces_of_many_requests(batch, rows, vocab, dt):
     # 511, 512 and 513 pieces of 8,192
     check(batch, rows, vocab, dt=dt, seed=batch)
+
+
+@pytest.mark.parametrize("rows,vocab", [(31, 8192), (32, 8192), (33, 8192), (8, 24577),
+                                        (7, 32768), (40, 2048), (40, 2049)])
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_few_pieces_of_one_request(rows, vocab, dt):
+    # 31, 32 and 33 pieces of 8,192, 32 and 28 of several a row; rows of one
+    # short piece and of one more logit
+    check(1, rows, vocab, dt=dt, accept=0.95, seed=rows)
 
 
 @pytest.mark.parametrize("dt", ["f16", "f32"])
