@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;   // head_dim 256
 constexpr int kSpan = 64;        // positions of a V tile
 constexpr int kPad = 2;          // elements between rows of the V tile
+constexpr int64_t kManyRows = 1536;  // from which on a workgroup takes 4 of them
 
 typedef uint32_t U4 __attribute__((ext_vector_type(4)));
 
@@ -333,8 +334,14 @@ hipError_t launch_cells(const KvAppendArgs &a, hipStream_t s)
         hipLaunchKernelGGL((append_elements<T, C>), dim3((uint32_t)rows), dim3(kThreads), 0, s, a);
         return hipGetLastError();
     }
-    // 4 rows a workgroup share its start once there are enough of them
-    const int R = rows > 2048 ? 4 : 1;
+    // 4 rows a workgroup share its start once there are enough of them. Measured,
+    // 1 and 4 rows (rows of the padded blocks, 16 a request; q, k and v heads):
+    // 512 rows of 64 + 8 + 8: 8.8 and 11.9 us, of 32 + 8 + 8: 7.7 and 8.0; 1,024:
+    // 13.6 and 13.7, 11.5 and 10.5; 1,536: 17.2 and 15.7, 14.8 and 14.5; 2,048: 21.0
+    // and 18.9, 17.8 and 17.2. One long block: 1,024 rows of 64 + 8 + 8 11.3 and 13.4,
+    // 1,536 15.1 and 15.4, 2,048 16.9 and 16.9; of 32 + 8 + 8 9.6 and 8.3, 12.4 and
+    // 10.3, 13.8 and 11.2.
+    const int R = rows >= kManyRows ? 4 : 1;
     const int64_t turning = (int64_t)g.batch * ((g.rows + R - 1) / R);
     const int64_t tiles = (g.rows + kSpan - 2) / kSpan + 1;
     const int64_t storing = (int64_t)g.batch * g.kv_heads * tiles;

@@ -40,9 +40,10 @@ def test_in_place_without_q_and_strided():
     check(LENGTHS, DLEN, ROWS, hq=2, hk=1, pad=3, offset=1, seed=55)
 
 
-@pytest.mark.parametrize("batch,rows", [(4, 512), (3, 683), (683, 3), (2050, 1)])
+@pytest.mark.parametrize("batch,rows", [(4, 512), (3, 683), (683, 3), (2050, 1), (5, 307),
+                                        (96, 16), (29, 53)])
 def test_both_sides_of_four_rows(batch, rows):
-    # 2,048, 2,049 and 2,050 rows
+    # 2,048 rows and some more; 1,535, 1,536 and 1,537
     rng = np.random.default_rng([9102, rows])
     dlen = rng.integers(-1, min(rows, 20), batch)
     check(rng.integers(0, 40, batch).tolist(), dlen.tolist(), rows, hq=1, hk=1, seed=rows)
