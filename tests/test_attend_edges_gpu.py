@@ -1,6 +1,7 @@
 """pld_attend (HIP, gfx950) at the edges of its arguments: scales so small
-that they vanish in 32 bits, and results in q's place. Tolerances are
-test_attend_gpu.py's."""
+that they vanish in 32 bits, results in q's place, the loosest bound on
+lengths, and more requests than the workspace holds partial results for.
+Tolerances are test_attend_gpu.py's."""
 
 from __future__ import annotations
 
@@ -58,3 +59,23 @@ def test_out_over_strided_q_is_refused():
         assert B.pld_sync(ctx) == B.PLD_OK and torch.equal(c.q, kept)
     finally:
         B.pld_destroy(ctx)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 20])
+@pytest.mark.parametrize("window", [0, 50])
+def test_the_largest_bound_on_lengths(rows, window):
+    c = Case([700, 9, 5000], [rows - 1, 0, rows // 2], rows, hq=8, hk=2, page=256, seed=23)
+    ctx = c.context(max_len=2**30)
+    try:
+        for max_len in (0, 2**30 - 7, c.max_len):
+            out, lse = c.outputs()
+            c.call(ctx, out, lse, window, max_len=max_len)
+            assert B.pld_sync(ctx) == B.PLD_OK
+            c.compare(out, lse, window)
+    finally:
+        B.pld_destroy(ctx)
+
+
+def test_more_requests_than_workgroups_to_split_among():
+    lengths = [1 + 37 * i % 600 for i in range(1500)]
+    check(lengths, [i % 3 - 1 for i in range(1500)], 2, hq=8, hk=4, seed=24)

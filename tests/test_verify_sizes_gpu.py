@@ -108,6 +108,11 @@ def test_vocabularies_of_more_than_4096_units(dt):
         B.pld_destroy(ctx)
 
 
+def test_many_requests_of_a_small_vocabulary():
+    check(5000, 3, 97, dt="bf16", seed=38, temperature=np.tile([1.0, 0.0], 2500),
+          dlen=[2, 1, 0, -1, 2] * 1000)
+
+
 def test_two_contexts_on_two_streams_at_once():
     """Each context's workspace is its own: calls overlapping on two streams,
     then captured into two graphs that replay at the same time, give what
