@@ -503,8 +503,8 @@ __device__ __forceinline__ void store_ml(const AttendArgs &a, const Split &sp, c
 // Up to 32 query rows: every wavefront holds all of them and takes tiles of
 // its own in turn; K and V go from HBM into its registers. Bound by HBM: 64
 // requests of 8,192 to 65,536 positions, 8 kv heads of 128 dims, one row of 4
-// query heads a kv head: 1.82 ms, 5.3 TB/s of bf16 cache (a plain streaming
-// read reaches 6.3).
+// query heads a kv head: 1.75 to 1.89 ms over six runs, 5.1 to 5.5 TB/s of bf16
+// cache (a plain streaming read reaches 6.3).
 template <typename T, typename C, int D, int MB>
 struct Narrow : Tiles<T, C, D, MB> {
     typedef Tiles<T, C, D, MB> S;
@@ -700,9 +700,9 @@ __global__ __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) void attend_narrow
 // (direct loads, in the order of the matrix operands: 1 KB each, read back
 // lane by lane). A ring of kStages tiles is in flight; one barrier a tile.
 // Bound by HBM with matrix and vector work in half of the cycles: 16 requests
-// of 262,144 positions, 2 kv heads of 128 dims, 128 query rows each: 0.89 ms,
-// 4.9 TB/s, 621 TFLOP/s; 2.00 ms when every wavefront held 64 rows and the
-// cache was read by two workgroups.
+// of 262,144 positions, 2 kv heads of 128 dims, 128 query rows each: 0.88 to 0.95
+// ms over six runs, 4.5 to 4.9 TB/s, 578 to 627 TFLOP/s; 2.00 ms when every
+// wavefront held 64 rows and the cache was read by two workgroups.
 template <typename T, typename C, int D, int RB>
 struct Wide : Tiles<T, C, D, RB> {
     typedef Tiles<T, C, D, RB> S;

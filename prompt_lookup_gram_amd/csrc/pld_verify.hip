@@ -209,8 +209,8 @@ __device__ __forceinline__ double sum_again(const T *z, int32_t vocab, float m, 
 
 // One workgroup per piece of a row, W 16-byte words a thread.
 // Measured: 64 requests of up to 16 draft tokens, 151,936 bf16 logits a row:
-// 37 us, 125 MB read where 62 are up to the refusals; one request of 17 rows of
-// 32,000: 7.7 us, the chain of its round trips.
+// 33 us, 121 MB read where 57 are up to the refusals; one request of 17 rows of
+// 32,000: 7.1 us, the chain of its round trips.
 // (8 wavefronts a SIMD: the rare second sum must not cost the first its
 // registers)
 template <typename T, int W>
@@ -481,7 +481,7 @@ __device__ __forceinline__ double weight_of(float z, int32_t i, double top, doub
 // kWaves units a workgroup. EXCESS 0: sums of the weights; the last workgroup
 // of a request without q at that row draws. EXCESS 1 (a second launch, when
 // there are drafter probabilities): sums of the excess over q, whose total of
-// the weights the first launch left. Measured: 31 us for 64 rows of 151,936
+// the weights the first launch left. Measured: 32 us for 64 rows of 151,936
 // logits (12 of them the 64-bit exponentials, 9.7 million), 12 us for one of
 // 32,000.
 template <typename T, int EXCESS, int E>
@@ -729,7 +729,7 @@ hipError_t launch_typed(const VerifyArgs &a, hipStream_t s)
                                pieces_of(a.vocab, kMinPiece), s);
     // units of 2,048 logits to draw from, or of 512 while they are few and a
     // unit's exponentials are what is waited for (the call, two rows a request:
-    // 0.14 million logits 19.5 us with 512, 24.7 with 2,048; 1.2 million 37.5 and
+    // 0.15 million logits 19.5 us with 512, 24.7 with 2,048; 1.2 million 37.5 and
     // 37.9; 1.6 million 31.7 and 31.2; 2.4 million 35.1 and 30.2; 9.7 million 72.5
     // and 45.0)
     if (e == hipSuccess)
