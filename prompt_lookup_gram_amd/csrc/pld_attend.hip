@@ -1004,7 +1004,8 @@ hipError_t launch_split(const AttendArgs &a, F kernel, hipStream_t s)
     sp.ml = (float2 *)(a.ws + a.ws_rows * D);
     const int64_t chunks = ceil_div((int64_t)g.batch * g.kv_heads * splits, 8) * 8;
     const int64_t joins = (int64_t)g.batch * g.rows * g.q_heads;
-    if (chunks * sp.m_tiles > 0x7fffffffLL || joins > 0x7fffffffLL)
+    if (!fits_grid(chunks * sp.m_tiles, kWaves * kWave) ||
+        (splits > 1 && !fits_grid(joins, kWave)))
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(kernel, dim3((uint32_t)(chunks * sp.m_tiles)), dim3(kWaves * kWave), 0, s,
                        a, sp);

@@ -331,6 +331,8 @@ hipError_t launch_cells(const KvAppendArgs &a, hipStream_t s)
                        !((a.q ? a.q_stride : 0) & 7) && !(a.kv_stride & 7) &&
                        a.rot_dim % (a.interleaved ? 8 : 16) == 0;
     if (!words) {
+        if (!fits_grid(rows, kThreads))
+            return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((append_elements<T, C>), dim3((uint32_t)rows), dim3(kThreads), 0, s, a);
         return hipGetLastError();
     }
@@ -345,7 +347,7 @@ hipError_t launch_cells(const KvAppendArgs &a, hipStream_t s)
     const int64_t turning = (int64_t)g.batch * ((g.rows + R - 1) / R);
     const int64_t tiles = (g.rows + kSpan - 2) / kSpan + 1;
     const int64_t storing = (int64_t)g.batch * g.kv_heads * tiles;
-    if (turning + storing > 0x7fffffffLL)
+    if (!fits_grid(turning + storing, kThreads))
         return hipErrorInvalidConfiguration;
     const size_t turn_lds = (size_t)R * (kMaxPairs * sizeof(float2) + sizeof(int32_t));
     const size_t tile_lds = (size_t)kSpan * (g.head_dim + kPad) * sizeof(T);

@@ -80,6 +80,10 @@ struct VerifyArgs {
     int32_t max_batch, max_rows;
 };
 
+// Whether one launch can have so many workgroups: the hardware counts a grid in
+// threads, in 32 bits.
+inline bool fits_grid(int64_t groups, int64_t threads) { return groups <= 0xffffffffLL / threads; }
+
 // What pld_create_target adds to a context.
 struct Target {
     pld_target_params p;

@@ -692,7 +692,7 @@ template <typename K>
 hipError_t start(K kernel, int threads, const VerifyArgs &a, const Space &sp, int64_t groups,
                  int64_t pieces, hipStream_t s)
 {
-    if (groups * pieces > 0x7fffffffLL)
+    if (!fits_grid(groups * pieces, threads))
         return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(kernel, dim3((uint32_t)(groups * pieces)), dim3(threads), 0, s, a, sp,
                        pieces);

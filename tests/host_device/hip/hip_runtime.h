@@ -60,6 +60,8 @@ struct State {
     std::function<void()> body;
     std::vector<int> order;        // of the wavefronts; those not named come last
     int64_t broken_barriers = 0, stuck = 0;
+    bool dry = false;              // launches are only looked at
+    uint64_t most_threads = 0;     // of any launch's grid
     std::function<void(const void *)> on_load;  // before an atomic load
 };
 
@@ -159,6 +161,9 @@ inline void run_block()
 inline void launch(uint32_t blocks, uint32_t threads, std::function<void()> body)
 {
     State &s = state();
+    s.most_threads = std::max(s.most_threads, (uint64_t)blocks * threads);
+    if (s.dry)
+        return;
     s.body = std::move(body);
     s.threads = threads;
     s.blocks = blocks;
@@ -254,7 +259,9 @@ struct dim3 {
 #define __global__
 #define __forceinline__ inline
 #define __launch_bounds__(...)
+#ifndef __shared__
 #define __shared__ static
+#endif
 #define threadIdx host_device::thread_idx()
 #define blockIdx host_device::block_idx()
 #define blockDim host_device::block_dim()
@@ -272,6 +279,11 @@ struct dim3 {
 #define __hip_atomic_fetch_min(p, v, order, scope) host_fetch_min(p, v)
 #define __builtin_amdgcn_exp2f(x) exp2f(x)
 #define __builtin_amdgcn_readfirstlane(x) host_first(x)
+inline void sincospif(float x, float *s, float *c)
+{
+    *s = (float)sin(M_PI * (double)x);
+    *c = (float)cos(M_PI * (double)x);
+}
 // (8-bit conversions: not run here)
 #define __builtin_amdgcn_cvt_f32_fp8(x, i) (abort(), (float)(x))
 #define __builtin_amdgcn_cvt_pk_fp8_f32(a, b, c, d) (abort(), (int)(a))

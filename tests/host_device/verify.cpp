@@ -27,6 +27,25 @@ int host_counters_clear(void *ws, int32_t batch, int32_t rows, int32_t vocab)
     return 1;
 }
 
+// The launches of a call of these sizes, not run: the threads of the largest
+// grid, or 0 where the sizes are refused.
+uint64_t host_verify_grid(int32_t batch, int32_t rows, int32_t vocab, int32_t dtype, int32_t head)
+{
+    pld::VerifyArgs a;
+    memset(&a, 0, sizeof(a));
+    a.dtype = dtype;
+    a.rows = a.max_rows = rows;
+    a.batch = a.max_batch = batch;
+    a.vocab = vocab;
+    a.head = head;
+    host_device::State &s = host_device::state();
+    s.dry = true;
+    s.most_threads = 0;
+    const hipError_t e = pld::launch_verify(a, nullptr);
+    s.dry = false;
+    return e == hipSuccess ? s.most_threads : 0;
+}
+
 // order: the wavefronts' order, `waves` of them. refuse_row > 0: `refuse_row`
 // is refused by another workgroup between the looks that two wavefronts of a
 // workgroup take at `stop`: the first finds no refusal, the others find it.

@@ -1,5 +1,6 @@
-"""pld_verify's kernels on the host, one workgroup at a time, in a chosen
-order of its wavefronts (tests/host_device). Arrays are numpy's."""
+"""pld_verify's and pld_kv_append's kernels on the host, one workgroup at a
+time, in a chosen order of its wavefronts (tests/host_device). Arrays are
+numpy's."""
 
 from __future__ import annotations
 
@@ -16,7 +17,7 @@ F32, F16, BF16 = 0, 1, 2
 BAD_BLOCK = 256
 ORDERS = [(0, 1, 2, 3), (3, 2, 1, 0), (2, 0, 3, 1), (1, 3, 0, 2)]
 
-vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 
 
 class Args(ctypes.Structure):
@@ -26,6 +27,22 @@ class Args(ctypes.Structure):
                 ("head", i32), ("temperature", vp), ("uniform", vp), ("out_tokens", vp),
                 ("out_accepted", vp), ("out_counts", vp), ("out_logprobs", vp), ("err", vp),
                 ("stats", vp), ("max_batch", i32), ("max_rows", i32)]
+
+
+class BlockArgs(ctypes.Structure):
+    """BlockArgs of pld_target.h."""
+    _fields_ = [("lengths", vp), ("draft_len", vp), ("rows", i32), ("batch", i32),
+                ("max_len", i32), ("table", vp), ("table_stride", i64), ("n_pages", i64),
+                ("page_shift", i32), ("q_heads", i32), ("kv_heads", i32), ("head_dim", i32),
+                ("dtype", i32), ("cache_dtype", i32), ("k_scale", vp), ("v_scale", vp),
+                ("err", vp)]
+
+
+class KvArgs(ctypes.Structure):
+    """KvAppendArgs of pld_target.h."""
+    _fields_ = [("blk", BlockArgs), ("q", vp), ("q_stride", i64), ("k", vp), ("v", vp),
+                ("kv_stride", i64), ("k_cache", vp), ("v_cache", vp), ("out_q", vp),
+                ("turns", vp), ("rot_dim", i32), ("interleaved", i32), ("magnitude", f32)]
 
 
 def build(folder, source="verify.cpp"):
@@ -42,6 +59,12 @@ def build(folder, source="verify.cpp"):
         out.host_workspace.argtypes = [i32, i32, i32]
         out.host_clear.argtypes = out.host_counters_clear.argtypes = [vp, i32, i32, i32]
         out.host_verify.argtypes = [ctypes.POINTER(Args), vp, i32, i32, vp]
+        out.host_verify_grid.restype = ctypes.c_uint64
+        out.host_verify_grid.argtypes = [i32] * 5
+    else:
+        out.host_kv_append.argtypes = [ctypes.POINTER(KvArgs), vp, i32, vp]
+        out.host_kv_grid.restype = ctypes.c_uint64
+        out.host_kv_grid.argtypes = [i32] * 4
     return out
 
 

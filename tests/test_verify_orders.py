@@ -173,3 +173,17 @@ def test_more_units_than_two_steps_of_a_wavefront_find(lib):
         assert abs(int(tok[b, 0]) - want) <= 1
         assert abs(logp[b, 0] - (z64[b, 0, tok[b, 0]] - z64[b, 0].max() - np.log(c[-1]))) <= (
             2.0**-17 + 2.0**-23 * 20)
+
+
+@pytest.mark.parametrize("dtype", [H.F32, H.F16, H.BF16])
+def test_grids_fit_the_hardwares_count_of_threads(lib, dtype):
+    """A grid is counted in threads, in 32 bits: sizes beyond are refused."""
+    ran = 0
+    for batch, rows, vocab, head in [
+            (1, 1, 1, 0), (64, 17, 151936, 0), (2**24 - 1, 1, 100, 0), (2**24, 1, 100, 0),
+            (2**20, 15, 100, 0), (2**20, 17, 100, 0), (2**30, 1, 1, 0), (2**20, 1, 151936, 0),
+            (2**15, 4, 2**24, 1), (1, 2**24, 2048, 0), (2**12, 2**12, 9000, 3)]:
+        threads = lib.host_verify_grid(batch, rows, vocab, dtype, head)
+        assert threads < 2**32, (batch, rows, vocab)
+        ran += threads > 0
+    assert ran == 4
