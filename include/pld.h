@@ -607,6 +607,9 @@ pld_status pld_draft_control_batch(pld_ctx *ctx, const int32_t *const *histories
  * rows; pld_verify commits nothing (its contract).
  */
 
+/* Nodes of a drafted tree, its root included, that a call takes. */
+#define PLD_TREE_ROWS 256
+
 /* element types */
 #define PLD_F32 0
 #define PLD_F16 1
@@ -817,6 +820,135 @@ pld_status pld_verify(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
                       int32_t *out_counts, float *out_logprobs, hipStream_t stream);
 
 /*
+ * A tree of drafted tokens: several continuations of a history verified in
+ * one pass. Its calls stand beside those of a chain: pld_kv_append_tree for
+ * pld_kv_append, pld_attend_tree for pld_attend, pld_verify_tree for
+ * pld_verify, and pld_kv_keep after it.
+ *
+ * A request's tree has n = 1 + d nodes: node 0, the root, is the history's last
+ * token, node t >= 1 is draft token t - 1 below node parent[t - 1]. Parents
+ * come before their children: 0 <= parent[t - 1] < t. A node's children are
+ * tried in the order of their indexes. Node t has row t of the block and cell
+ * L - 1 + t of the cache, and stands at position L - 1 + its depth. lengths,
+ * draft_len, rows and padding are as in a block; rows is at most
+ * PLD_TREE_ROWS.
+ *  parent: device int32 [batch][rows - 1], or NULL: chains (parent[t - 1] =
+ *          t - 1), whose results are the chain calls'.
+ * Bad inputs are those of a block, and a parent of a node t <= d outside [0, t),
+ * which sets PLD_EINVAL; entries past d are not read.
+ *
+ * A step: the drafters' tokens and parents; per layer pld_kv_append_tree and
+ * pld_attend_tree; pld_verify_tree; pld_kv_keep of every layer; pld_append of
+ * its tokens (which moves the store's lengths on: pld_kv_keep comes before).
+ */
+
+/*
+ * pld_kv_append of a tree's rows, with the norms that a model has on the heads
+ * of its queries and keys: each q and k head x of head_dim elements becomes
+ *   x[i] * norm[i] / sqrt(mean of x^2 + eps),
+ * then the row is rotated at its position (L - 1 + depth) and its k and v go
+ * to cell L - 1 + t. Norm and rotation are held in 32 bits, and the result is
+ * rounded once.
+ *  parent: as above; with NULL, rows may be any that pld_kv_append takes (a
+ *          prompt of a model with norms).
+ *  q_norm, k_norm: device float[head_dim], or NULL: no norm on q, on k.
+ *  eps:    >= 0, finite.
+ * Everything else as in pld_kv_append. A request with a bad parent has no rows.
+ * Errors: PLD_EINVAL, PLD_EHIP.
+ */
+pld_status pld_kv_append_tree(pld_ctx *ctx, const void *q, int64_t q_stride, const void *k,
+                              const void *v, int64_t kv_stride, int32_t rows,
+                              const int32_t *lengths, const int32_t *draft_len,
+                              const int32_t *parent, int32_t batch, const int32_t *page_table,
+                              int64_t table_stride, void *k_cache, void *v_cache,
+                              int64_t n_pages, const float *k_scale, const float *v_scale,
+                              const float *q_norm, const float *k_norm, float eps, void *out_q,
+                              hipStream_t stream);
+
+/*
+ * pld_attend of a tree's rows: row t sees the cells j <= L - 1 (the history and
+ * the root) and, of the tree, its ancestors' cells and its own. With a window
+ * it sees those of them with p_j > p_t - window, p_j being a cell's position:
+ * j up to the root, L - 1 + depth behind it.
+ *  parent: as above; with NULL, rows may be any that pld_attend takes.
+ * Everything else as in pld_attend. The rows of a request with a bad parent are
+ * written as NaN (the root's row may hold its values).
+ * Errors: PLD_EINVAL, PLD_EHIP.
+ */
+pld_status pld_attend_tree(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t rows,
+                           const int32_t *lengths, const int32_t *draft_len,
+                           const int32_t *parent, int64_t max_len, int32_t batch,
+                           const int32_t *page_table, int64_t table_stride, const void *k_cache,
+                           const void *v_cache, int64_t n_pages, const float *k_scale,
+                           const float *v_scale, float scale, int32_t window, void *out,
+                           float *out_lse, hipStream_t stream);
+
+/*
+ * Verification of a tree against the target model's logits, from given random
+ * numbers. Logits row t belongs to node t and gives p_t = softmax(z_t / T) for
+ * the token after it.
+ *
+ * The walk starts at the root. At node v, with R = 1, its children are tried in
+ * index order: child c with token x is accepted when
+ *   u_c R < p_v(x)
+ * (u_c: the uniform of node c); the walk then goes on at c. A refused child's
+ * token is out: R -= p_v(x), and the same token below v once more is refused.
+ * Where no child is accepted (a leaf has none) one token is drawn from p_v
+ * without the refused tokens, as pld_verify draws. This commits tokens
+ * distributed as the target's own samples: a drafted token is a point mass, tried
+ * with what the tries before it left. T = 0 is greedy: the first child that
+ * is the row's argmax (lowest index on a tie) is accepted, and at the end the
+ * argmax is committed; u is not used. On a chain the results are pld_verify's
+ * without draft_probs.
+ *
+ *  logits, logits_dtype, logits_stride, rows, draft, draft_len, temperature,
+ *            uniform, batch, out_tokens, out_counts: as in pld_verify (node t's
+ *            uniform is column t - 1); out_tokens are the path's tokens and the
+ *            drawn one, what pld_append takes.
+ *  parent:   as above.
+ *  out_path: device int32 [batch][rows]: the nodes of the accepted path, 0 (the
+ *            root) first, -1 past it.
+ *  out_accepted: device int32[batch], a: accepted drafted nodes.
+ *  out_logprobs: device float [batch][rows] or NULL: ln p of each committed token
+ *            at its row (at T = 1 for greedy requests), 0 past them.
+ * d = -1: no tokens, a path of -1, a = 0 and count 0. Rows off the path need not be
+ * read and are not checked. A request is written like d = -1 and sets the
+ * sticky flag (PLD_EINVAL) for a bad parent and for what pld_verify refuses.
+ * Errors: PLD_EINVAL, PLD_EHIP.
+ */
+pld_status pld_verify_tree(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
+                           int64_t logits_stride, int32_t rows, const int32_t *draft,
+                           const int32_t *draft_len, const int32_t *parent,
+                           const float *temperature, const float *uniform, int32_t batch,
+                           int32_t *out_tokens, int32_t *out_path, int32_t *out_accepted,
+                           int32_t *out_counts, float *out_logprobs, hipStream_t stream);
+
+/*
+ * The accepted path's keys and values, moved side by side: cell L - 1 + path[i]
+ * goes to cell L - 1 + i for i = 1..accepted, in every layer and kv head, so that
+ * the cache holds the committed tokens' cells in order (the drawn token's come
+ * with the next block). Cells are moved as they are stored; cells behind the
+ * last one moved keep what they hold.
+ *  lengths, draft_len: the block's, as the tree's other calls had them (before
+ *            pld_append moves the lengths on).
+ *  path, accepted: pld_verify_tree's out_path [batch][rows] and out_accepted.
+ *  rows:     1 <= rows <= max_rows, at most PLD_TREE_ROWS.
+ *  k_cache, v_cache, n_pages: the first layer's caches.
+ *  layers:   >= 0 layers, each k_layer_stride and v_layer_stride elements behind
+ *            the one before it (multiples of 16 bytes, each >= a layer's cache; not
+ *            used with one layer); 0 is a no-op.
+ * Nothing of a request is moved, and the sticky flag is set, when its block, its
+ * path (path[0] = 0, rising, at most d; accepted within [0, d]) or a page that a
+ * move needs is bad. accepted = 0 moves nothing, whatever path holds.
+ * Errors: PLD_EINVAL, PLD_EHIP.
+ */
+pld_status pld_kv_keep(pld_ctx *ctx, const int32_t *lengths, const int32_t *draft_len,
+                       const int32_t *path, const int32_t *accepted, int32_t rows, int32_t batch,
+                       const int32_t *page_table, int64_t table_stride, void *k_cache,
+                       void *v_cache, int64_t n_pages, int32_t layers, int64_t k_layer_stride,
+                       int64_t v_layer_stride, hipStream_t stream);
+
+/*
  * Wait for the device (the given stream and every other stream), then
  * report and clear the sticky device-side flag. The flag exists so that a
  * bad request is reported and never silently cut short (the Strata engine
@@ -827,8 +959,8 @@ pld_status pld_verify(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
  * was negative, a length was below a strided call's min_len, a row pointer
  * was null or misaligned, pld_fuse saw inconsistent per-request inputs,
  * pld_control an outcome out of range, or a verify-step call a bad block,
- * page id, token, temperature, random number or logit (capacity wins when
- * both are set).
+ * page id, parent, path, token, temperature, random number or logit (capacity
+ * wins when both are set).
  * Errors: PLD_EINVAL (null ctx), PLD_EHIP.
  */
 pld_status pld_sync(pld_ctx *ctx, hipStream_t stream);

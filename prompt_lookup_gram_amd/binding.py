@@ -37,7 +37,7 @@ EXPORTS = ("pld_create", "pld_create_indexed", "pld_destroy", "pld_configure", "
            "pld_ngram_params_default", "pld_create_ngram", "pld_draft_ngram",
            "pld_append_draft_ngram", "pld_draft_control_batch",
            "pld_target_params_default", "pld_create_target", "pld_kv_append", "pld_attend",
-           "pld_verify",
+           "pld_verify", "pld_kv_append_tree", "pld_attend_tree", "pld_verify_tree", "pld_kv_keep",
            "pld_sync", "pld_strerror",
            "pld_last_error")
 
@@ -165,6 +165,13 @@ def load(path: str = LIB_PATH):
                        ctypes.c_float, i32, vp, vp, vp],
         "pld_verify": [vp, vp, i32, i64, i32, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp,
                        vp],
+        "pld_kv_append_tree": [vp, vp, i64, vp, vp, i64, i32, vp, vp, vp, i32, vp, i64, vp, vp,
+                               i64, vp, vp, vp, vp, ctypes.c_float, vp, vp],
+        "pld_attend_tree": [vp, vp, i64, i32, vp, vp, vp, i64, i32, vp, i64, vp, vp, i64, vp, vp,
+                            ctypes.c_float, i32, vp, vp, vp],
+        "pld_verify_tree": [vp, vp, i32, i64, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp,
+                            vp],
+        "pld_kv_keep": [vp, vp, vp, vp, vp, i32, i32, vp, i64, vp, vp, i64, i32, i64, i64, vp],
         "pld_sync": [vp, vp],
     }
     for name, args in sig.items():
@@ -652,6 +659,94 @@ def pld_verify(ctx: int, logits, logits_stride: int, rows: int, draft, draft_len
         _stream(stream))
     if st:
         _check("pld_verify", st)
+
+
+def pld_kv_append_tree(ctx: int, q, q_stride: int, k, v, kv_stride: int, rows: int, lengths,
+                       draft_len, parent, batch: int, page_table, table_stride: int, k_cache,
+                       v_cache, n_pages: int, k_scale=None, v_scale=None, q_norm=None, k_norm=None,
+                       eps: float = 0.0, out_q=None, stream=None) -> None:
+    """Norms of the heads of q and k, rotary positions by depth, and the
+    tree's keys and values into the paged cache (include/pld.h). `parent` is
+    None for chains and prompts; q_norm and k_norm are float32 weights of
+    head_dim elements, or None."""
+    t = _types or _verify_types()
+    dev, i32, f32 = _device(t), t["i32"], t["f32"]
+    half, cells = _target_dtypes(t, ctx)
+    st = (_lib or load()).pld_kv_append_tree(
+        ctx, _rows_arg(q, "q", half, dev), int(q_stride), _rows_arg(k, "k", half, dev),
+        _rows_arg(v, "v", half, dev), int(kv_stride), int(rows),
+        _arg(lengths, "lengths", i32, dev), _arg(draft_len, "draft_len", i32, dev),
+        _arg(parent, "parent", i32, dev), int(batch),
+        _arg(page_table, "page_table", i32, dev), int(table_stride),
+        _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev),
+        int(n_pages), _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev),
+        _arg(q_norm, "q_norm", f32, dev), _arg(k_norm, "k_norm", f32, dev), float(eps),
+        _arg(out_q, "out_q", half, dev), _stream(stream))
+    if st:
+        _check("pld_kv_append_tree", st)
+
+
+def pld_attend_tree(ctx: int, q, q_stride: int, rows: int, lengths, draft_len, parent,
+                    max_len: int, batch: int, page_table, table_stride: int, k_cache, v_cache,
+                    n_pages: int, k_scale=None, v_scale=None, scale: float = 0.0,
+                    window: int = 0, out=None, out_lse=None, stream=None) -> None:
+    """Attention of a tree's rows over the paged cache (include/pld.h).
+    `parent` is None for chains."""
+    t = _types or _verify_types()
+    dev, i32, f32 = _device(t), t["i32"], t["f32"]
+    half, cells = _target_dtypes(t, ctx)
+    st = (_lib or load()).pld_attend_tree(
+        ctx, _rows_arg(q, "q", half, dev), int(q_stride), int(rows),
+        _arg(lengths, "lengths", i32, dev), _arg(draft_len, "draft_len", i32, dev),
+        _arg(parent, "parent", i32, dev), int(max_len), int(batch),
+        _arg(page_table, "page_table", i32, dev), int(table_stride),
+        _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev), int(n_pages),
+        _arg(k_scale, "k_scale", f32, dev), _arg(v_scale, "v_scale", f32, dev), float(scale),
+        int(window), _arg(out, "out", half, dev), _arg(out_lse, "out_lse", f32, dev),
+        _stream(stream))
+    if st:
+        _check("pld_attend_tree", st)
+
+
+def pld_verify_tree(ctx: int, logits, logits_stride: int, rows: int, draft, draft_len, parent,
+                    temperature, uniform, batch: int, out_tokens, out_path, out_accepted,
+                    out_counts, out_logprobs=None, stream=None) -> None:
+    """Verification of a tree of drafted tokens (include/pld.h). `logits` and
+    `temperature` as in pld_verify; `parent` is None for chains."""
+    t = _types or _verify_types()
+    dev, i32, f32, types = _device(t), t["i32"], t["f32"], t["logits"]
+    if not isinstance(logits, t["tensor"]):
+        raise TypeError("logits: expected a torch tensor")
+    ptr = _rows_arg(logits, "logits", types, dev)
+    st = (_lib or load()).pld_verify_tree(
+        ctx, ptr, types[logits.dtype], int(logits_stride), int(rows),
+        _arg(draft, "draft", i32, dev), _arg(draft_len, "draft_len", i32, dev),
+        _arg(parent, "parent", i32, dev), _arg(temperature, "temperature", f32, dev),
+        _arg(uniform, "uniform", f32, dev), int(batch), _arg(out_tokens, "out_tokens", i32, dev),
+        _arg(out_path, "out_path", i32, dev), _arg(out_accepted, "out_accepted", i32, dev),
+        _arg(out_counts, "out_counts", i32, dev), _arg(out_logprobs, "out_logprobs", f32, dev),
+        _stream(stream))
+    if st:
+        _check("pld_verify_tree", st)
+
+
+def pld_kv_keep(ctx: int, lengths, draft_len, path, accepted, rows: int, batch: int, page_table,
+                table_stride: int, k_cache, v_cache, n_pages: int, layers: int = 1,
+                k_layer_stride: int = 0, v_layer_stride: int = 0, stream=None) -> None:
+    """The accepted path's keys and values, moved side by side in every layer
+    (include/pld.h). k_cache and v_cache are the first layer's, or the whole
+    stack of layers."""
+    t = _types or _verify_types()
+    dev, i32 = _device(t), t["i32"]
+    cells = _target_dtypes(t, ctx)[1]
+    st = (_lib or load()).pld_kv_keep(
+        ctx, _arg(lengths, "lengths", i32, dev), _arg(draft_len, "draft_len", i32, dev),
+        _arg(path, "path", i32, dev), _arg(accepted, "accepted", i32, dev), int(rows), int(batch),
+        _arg(page_table, "page_table", i32, dev), int(table_stride),
+        _arg(k_cache, "k_cache", cells, dev), _arg(v_cache, "v_cache", cells, dev), int(n_pages),
+        int(layers), int(k_layer_stride), int(v_layer_stride), _stream(stream))
+    if st:
+        _check("pld_kv_keep", st)
 
 
 def pld_sync(ctx: int, stream=None) -> int:

@@ -37,13 +37,16 @@ def sources():
     return [os.path.join(CSRC, "pld_kernels.hip"), os.path.join(CSRC, "pld_index.hip"),
             os.path.join(CSRC, "pld_control.hip"), os.path.join(CSRC, "pld_ngram.hip"),
             os.path.join(CSRC, "pld_kv.hip"), os.path.join(CSRC, "pld_attend.hip"),
-            os.path.join(CSRC, "pld_verify.hip"), os.path.join(CSRC, "pld_target_api.cpp"),
+            os.path.join(CSRC, "pld_verify.hip"), os.path.join(CSRC, "pld_tree_kv.hip"),
+            os.path.join(CSRC, "pld_tree_attend.hip"), os.path.join(CSRC, "pld_tree_verify.hip"),
+            os.path.join(CSRC, "pld_target_api.cpp"),
             os.path.join(CSRC, "pld_api.cpp")]
 
 
 def build(verbose: bool = False) -> str:
     """Compile every source and link libpld.so; returns its path."""
-    objs = []
+    # (a process a source: the attention's kernels take a minute each)
+    objs, running = [], []
     for src in sources():
         obj = os.path.join(CSRC, os.path.basename(src) + ".o")
         lang = ["-x", "hip"] if src.endswith(".hip") else []
@@ -51,8 +54,13 @@ def build(verbose: bool = False) -> str:
                "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        running.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    for cmd, p in running:
+        p.wait()
+    for cmd, p in running:
+        if p.returncode:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:

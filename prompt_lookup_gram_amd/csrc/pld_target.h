@@ -57,6 +57,27 @@ struct AttendArgs {
     float *out_lse;            // or null
     float *ws;                 // workspace: partial results of ws_rows rows
     int64_t ws_rows;           // (head_dim floats each, then two floats each)
+    const int32_t *parent;     // trees: [batch][rows - 1]
+};
+
+// pld_kv_append_tree
+struct TreeAppendArgs {
+    KvAppendArgs kv;
+    const int32_t *parent;     // [batch][rows - 1], or null: chains
+    const float *q_norm;       // [head_dim], or null
+    const float *k_norm;
+    float eps;
+};
+
+// pld_kv_keep
+struct KeepArgs {
+    BlockArgs blk;
+    const int32_t *path;       // [batch][rows]
+    const int32_t *accepted;   // [batch]
+    void *k_cache;
+    void *v_cache;
+    int32_t layers;
+    int64_t k_layer, v_layer;  // elements between layers
 };
 
 struct VerifyArgs {
@@ -78,6 +99,13 @@ struct VerifyArgs {
     unsigned int *err;
     void *stats;               // workspace, for max_batch blocks of max_rows rows
     int32_t max_batch, max_rows;
+};
+
+// pld_verify_tree
+struct TreeVerifyArgs {
+    VerifyArgs v;              // (no src, probs and head)
+    const int32_t *parent;     // [batch][rows - 1], or null: chains
+    int32_t *out_path;         // [batch][rows]
 };
 
 // Whether one launch can have so many workgroups: the hardware counts a grid in
@@ -104,6 +132,10 @@ hipError_t verify_clear(void *ws, int32_t batch, int32_t rows, int32_t vocab, hi
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s);
 hipError_t launch_attend(const AttendArgs &a, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t s);
+hipError_t launch_kv_append_tree(const TreeAppendArgs &a, hipStream_t s);
+hipError_t launch_attend_tree(const AttendArgs &a, hipStream_t s);
+hipError_t launch_verify_tree(const TreeVerifyArgs &a, hipStream_t s);
+hipError_t launch_kv_keep(const KeepArgs &a, hipStream_t s);
 
 }  // namespace pld
 

@@ -1,6 +1,6 @@
 // C-ABI entry points of the verify step (include/pld.h): the target context,
-// argument checks and the launches of pld_kv.hip, pld_attend.hip and
-// pld_verify.hip. No compute happens here but the rotary frequencies, once
+// argument checks and the launches of pld_kv.hip, pld_attend.hip,
+// pld_verify.hip and their counterparts for trees. No compute happens here but the rotary frequencies, once
 // per context.
 
 #include <math.h>
@@ -189,6 +189,156 @@ pld_status block_args(pld_ctx *ctx, int32_t rows, const int32_t *lengths,
     return PLD_OK;
 }
 
+// The checks of a cache append; fills `a`.
+pld_status append_args(pld_ctx *ctx, const void *q, int64_t q_stride, const void *k,
+                       const void *v, int64_t kv_stride, int32_t rows, const int32_t *lengths,
+                       const int32_t *draft_len, int32_t batch, const int32_t *page_table,
+                       int64_t table_stride, void *k_cache, void *v_cache, int64_t n_pages,
+                       const float *k_scale, const float *v_scale, void *out_q,
+                       pld::KvAppendArgs &a)
+{
+    pld_status st = block_args(ctx, rows, lengths, draft_len, 0, batch, page_table, table_stride,
+                               k_cache, v_cache, n_pages, k_scale, v_scale, a.blk);
+    if (st != PLD_OK)
+        return st;
+    const pld_target_params &p = ctx->target->p;
+    const int64_t q_width = (int64_t)p.q_heads * p.head_dim;
+    const int64_t kv_width = (int64_t)p.kv_heads * p.head_dim;
+    if (batch > 0 && (!k || !v || (q != nullptr) != (out_q != nullptr)))
+        return fail(PLD_EINVAL, "k or v is null, or only one of q and out_q is");
+    if ((q && q_stride < q_width) || kv_stride < kv_width)
+        return fail(PLD_EINVAL, "q_stride and kv_stride must hold a row (%lld and %lld elements)",
+                    (long long)q_width, (long long)kv_width);
+    if (q && q == out_q && q_stride != q_width)
+        return fail(PLD_EINVAL, "q rotated in place needs q_stride %lld", (long long)q_width);
+    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)out_q) & 1u)
+        return fail(PLD_EINVAL, "q, k, v and out_q must be 2-byte aligned");
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k = k;
+    a.v = v;
+    a.kv_stride = kv_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.out_q = out_q;
+    a.turns = ctx->target->turns;
+    a.rot_dim = p.rope.rot_dim;
+    a.interleaved = p.rope.interleaved;
+    a.magnitude = (float)p.rope.magnitude;
+    return PLD_OK;
+}
+
+// The checks of an attention; fills `a`.
+pld_status attend_args(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t rows,
+                       const int32_t *lengths, const int32_t *draft_len, int64_t max_len,
+                       int32_t batch, const int32_t *page_table, int64_t table_stride,
+                       const void *k_cache, const void *v_cache, int64_t n_pages,
+                       const float *k_scale, const float *v_scale, float scale, int32_t window,
+                       void *out, float *out_lse, pld::AttendArgs &a)
+{
+    pld_status st = block_args(ctx, rows, lengths, draft_len, max_len, batch, page_table,
+                               table_stride, k_cache, v_cache, n_pages, k_scale, v_scale, a.blk);
+    if (st != PLD_OK)
+        return st;
+    const pld_target_params &p = ctx->target->p;
+    if (batch > 0 && (!q || !out))
+        return fail(PLD_EINVAL, "null buffer pointer");
+    if (q_stride < (int64_t)p.q_heads * p.head_dim || (q_stride & 7))
+        return fail(PLD_EINVAL, "q_stride must be a multiple of 8 elements and hold a row "
+                    "(got %lld)", (long long)q_stride);
+    if (((uintptr_t)q | (uintptr_t)out) & 15u)
+        return fail(PLD_EINVAL, "q and out must be 16-byte aligned");
+    if (q && q == out && q_stride != (int64_t)p.q_heads * p.head_dim)
+        return fail(PLD_EINVAL, "out in q's place needs q_stride %lld",
+                    (long long)p.q_heads * p.head_dim);
+    if ((uintptr_t)out_lse & 3u)
+        return fail(PLD_EINVAL, "out_lse must be 4-byte aligned");
+    if (!isfinite(scale))
+        return fail(PLD_EINVAL, "scale must be finite");
+    if (window < 0)
+        return fail(PLD_EINVAL, "window must be >= 0 (got %d)", window);
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.scale = scale != 0.0f ? scale : (float)(1.0 / sqrt((double)p.head_dim));
+    a.window = window;
+    a.out = out;
+    a.out_lse = out_lse;
+    a.ws = ctx->target->attend_ws;
+    a.ws_rows = ctx->target->attend_rows;
+    a.parent = nullptr;
+    return PLD_OK;
+}
+
+// The checks of a verification; fills `a`.
+pld_status verify_args(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
+                       int64_t logits_stride, int32_t rows, const int32_t *draft,
+                       const int32_t *draft_len, const uint64_t *src, const float *draft_probs,
+                       int32_t head, const float *temperature, const float *uniform,
+                       int32_t batch, int32_t *out_tokens, int32_t *out_accepted,
+                       int32_t *out_counts, float *out_logprobs, pld::VerifyArgs &a)
+{
+    pld_status st = check_call(ctx, rows, batch);
+    if (st != PLD_OK)
+        return st;
+    const pld_target_params &p = ctx->target->p;
+    if (p.vocab == 0)
+        return fail(PLD_EINVAL, "the context has no vocab (see pld_target_params)");
+    if (logits_dtype != PLD_F32 && logits_dtype != PLD_F16 && logits_dtype != PLD_BF16)
+        return fail(PLD_EINVAL, "logits_dtype must be PLD_F32, PLD_F16 or PLD_BF16 (got %d)",
+                    logits_dtype);
+    if (logits_stride < p.vocab)
+        return fail(PLD_EINVAL, "logits_stride %lld below the vocab %d", (long long)logits_stride,
+                    p.vocab);
+    if (head < 0 || head > rows - 1 || (head > 0) != (draft_probs != nullptr))
+        return fail(PLD_EINVAL, "head must be in [0, rows - 1], and > 0 exactly with draft_probs "
+                    "(got %d)", head);
+    if (batch > 0 && (!logits || !draft_len || !uniform || !out_tokens || !out_accepted ||
+                      !out_counts || (rows > 1 && !draft)))
+        return fail(PLD_EINVAL, "null buffer pointer");
+    if (((uintptr_t)draft | (uintptr_t)draft_len | (uintptr_t)draft_probs |
+         (uintptr_t)temperature | (uintptr_t)uniform | (uintptr_t)out_tokens |
+         (uintptr_t)out_accepted | (uintptr_t)out_counts | (uintptr_t)out_logprobs) & 3u)
+        return fail(PLD_EINVAL, "int32 and float buffers must be 4-byte aligned");
+    if ((uintptr_t)src & 7u)
+        return fail(PLD_EINVAL, "src must be 8-byte aligned");
+    if ((uintptr_t)logits & (logits_dtype == PLD_F32 ? 3u : 1u))
+        return fail(PLD_EINVAL, "logits must be aligned to their elements");
+    a.logits = logits;
+    a.dtype = logits_dtype;
+    a.stride = logits_stride;
+    a.rows = rows;
+    a.batch = batch;
+    a.vocab = p.vocab;
+    a.draft = draft;
+    a.draft_len = draft_len;
+    a.src = src;
+    a.probs = draft_probs;
+    a.head = head;
+    a.temperature = temperature;
+    a.uniform = uniform;
+    a.out_tokens = out_tokens;
+    a.out_accepted = out_accepted;
+    a.out_counts = out_counts;
+    a.out_logprobs = out_logprobs;
+    a.err = ctx->err;
+    a.stats = ctx->target->verify_ws;
+    a.max_batch = p.max_batch;
+    a.max_rows = p.max_rows;
+    return PLD_OK;
+}
+
+// The checks that a tree's calls add.
+pld_status tree_rows(int32_t rows, const int32_t *parent)
+{
+    if (rows > PLD_TREE_ROWS)
+        return fail(PLD_EINVAL, "rows %d: a tree has at most %d", rows, PLD_TREE_ROWS);
+    if ((uintptr_t)parent & 3u)
+        return fail(PLD_EINVAL, "parent must be 4-byte aligned");
+    return PLD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -283,36 +433,11 @@ pld_status pld_kv_append(pld_ctx *ctx, const void *q, int64_t q_stride, const vo
                          const float *v_scale, void *out_q, hipStream_t stream)
 {
     pld::KvAppendArgs a;
-    pld_status st = block_args(ctx, rows, lengths, draft_len, 0, batch, page_table, table_stride,
-                               k_cache, v_cache, n_pages, k_scale, v_scale, a.blk);
-    if (st != PLD_OK)
+    const pld_status st =
+        append_args(ctx, q, q_stride, k, v, kv_stride, rows, lengths, draft_len, batch, page_table,
+                    table_stride, k_cache, v_cache, n_pages, k_scale, v_scale, out_q, a);
+    if (st != PLD_OK || batch == 0)
         return st;
-    const pld_target_params &p = ctx->target->p;
-    const int64_t q_width = (int64_t)p.q_heads * p.head_dim;
-    const int64_t kv_width = (int64_t)p.kv_heads * p.head_dim;
-    if (batch > 0 && (!k || !v || (q != nullptr) != (out_q != nullptr)))
-        return fail(PLD_EINVAL, "k or v is null, or only one of q and out_q is");
-    if ((q && q_stride < q_width) || kv_stride < kv_width)
-        return fail(PLD_EINVAL, "q_stride and kv_stride must hold a row (%lld and %lld elements)",
-                    (long long)q_width, (long long)kv_width);
-    if (q && q == out_q && q_stride != q_width)
-        return fail(PLD_EINVAL, "q rotated in place needs q_stride %lld", (long long)q_width);
-    if (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)out_q) & 1u)
-        return fail(PLD_EINVAL, "q, k, v and out_q must be 2-byte aligned");
-    if (batch == 0)
-        return PLD_OK;
-    a.q = q;
-    a.q_stride = q_stride;
-    a.k = k;
-    a.v = v;
-    a.kv_stride = kv_stride;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.out_q = out_q;
-    a.turns = ctx->target->turns;
-    a.rot_dim = p.rope.rot_dim;
-    a.interleaved = p.rope.interleaved;
-    a.magnitude = (float)p.rope.magnitude;
     const hipError_t e = pld::launch_kv_append(a, stream);
     if (e != hipSuccess)
         return hip_fail(e, "cache append launch");
@@ -327,39 +452,12 @@ pld_status pld_attend(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t row
                       void *out, float *out_lse, hipStream_t stream)
 {
     pld::AttendArgs a;
-    pld_status st = block_args(ctx, rows, lengths, draft_len, max_len, batch, page_table,
-                               table_stride, k_cache, v_cache, n_pages, k_scale, v_scale, a.blk);
-    if (st != PLD_OK)
+    const pld_status st =
+        attend_args(ctx, q, q_stride, rows, lengths, draft_len, max_len, batch, page_table,
+                    table_stride, k_cache, v_cache, n_pages, k_scale, v_scale, scale, window, out,
+                    out_lse, a);
+    if (st != PLD_OK || batch == 0)
         return st;
-    const pld_target_params &p = ctx->target->p;
-    if (batch > 0 && (!q || !out))
-        return fail(PLD_EINVAL, "null buffer pointer");
-    if (q_stride < (int64_t)p.q_heads * p.head_dim || (q_stride & 7))
-        return fail(PLD_EINVAL, "q_stride must be a multiple of 8 elements and hold a row "
-                    "(got %lld)", (long long)q_stride);
-    if (((uintptr_t)q | (uintptr_t)out) & 15u)
-        return fail(PLD_EINVAL, "q and out must be 16-byte aligned");
-    if (q && q == out && q_stride != (int64_t)p.q_heads * p.head_dim)
-        return fail(PLD_EINVAL, "out in q's place needs q_stride %lld",
-                    (long long)p.q_heads * p.head_dim);
-    if ((uintptr_t)out_lse & 3u)
-        return fail(PLD_EINVAL, "out_lse must be 4-byte aligned");
-    if (!isfinite(scale))
-        return fail(PLD_EINVAL, "scale must be finite");
-    if (window < 0)
-        return fail(PLD_EINVAL, "window must be >= 0 (got %d)", window);
-    if (batch == 0)
-        return PLD_OK;
-    a.q = q;
-    a.q_stride = q_stride;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.scale = scale != 0.0f ? scale : (float)(1.0 / sqrt((double)p.head_dim));
-    a.window = window;
-    a.out = out;
-    a.out_lse = out_lse;
-    a.ws = ctx->target->attend_ws;
-    a.ws_rows = ctx->target->attend_rows;
     const hipError_t e = pld::launch_attend(a, stream);
     if (e != hipSuccess)
         return hip_fail(e, "attention launch");
@@ -373,59 +471,151 @@ pld_status pld_verify(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
                       int32_t batch, int32_t *out_tokens, int32_t *out_accepted,
                       int32_t *out_counts, float *out_logprobs, hipStream_t stream)
 {
-    pld_status st = check_call(ctx, rows, batch);
-    if (st != PLD_OK)
-        return st;
-    const pld_target_params &p = ctx->target->p;
-    if (p.vocab == 0)
-        return fail(PLD_EINVAL, "the context has no vocab (see pld_target_params)");
-    if (logits_dtype != PLD_F32 && logits_dtype != PLD_F16 && logits_dtype != PLD_BF16)
-        return fail(PLD_EINVAL, "logits_dtype must be PLD_F32, PLD_F16 or PLD_BF16 (got %d)",
-                    logits_dtype);
-    if (logits_stride < p.vocab)
-        return fail(PLD_EINVAL, "logits_stride %lld below the vocab %d", (long long)logits_stride,
-                    p.vocab);
-    if (head < 0 || head > rows - 1 || (head > 0) != (draft_probs != nullptr))
-        return fail(PLD_EINVAL, "head must be in [0, rows - 1], and > 0 exactly with draft_probs "
-                    "(got %d)", head);
-    if (batch > 0 && (!logits || !draft_len || !uniform || !out_tokens || !out_accepted ||
-                      !out_counts || (rows > 1 && !draft)))
-        return fail(PLD_EINVAL, "null buffer pointer");
-    if (((uintptr_t)draft | (uintptr_t)draft_len | (uintptr_t)draft_probs |
-         (uintptr_t)temperature | (uintptr_t)uniform | (uintptr_t)out_tokens |
-         (uintptr_t)out_accepted | (uintptr_t)out_counts | (uintptr_t)out_logprobs) & 3u)
-        return fail(PLD_EINVAL, "int32 and float buffers must be 4-byte aligned");
-    if ((uintptr_t)src & 7u)
-        return fail(PLD_EINVAL, "src must be 8-byte aligned");
-    if ((uintptr_t)logits & (logits_dtype == PLD_F32 ? 3u : 1u))
-        return fail(PLD_EINVAL, "logits must be aligned to their elements");
-    if (batch == 0)
-        return PLD_OK;
     pld::VerifyArgs a;
-    a.logits = logits;
-    a.dtype = logits_dtype;
-    a.stride = logits_stride;
-    a.rows = rows;
-    a.batch = batch;
-    a.vocab = p.vocab;
-    a.draft = draft;
-    a.draft_len = draft_len;
-    a.src = src;
-    a.probs = draft_probs;
-    a.head = head;
-    a.temperature = temperature;
-    a.uniform = uniform;
-    a.out_tokens = out_tokens;
-    a.out_accepted = out_accepted;
-    a.out_counts = out_counts;
-    a.out_logprobs = out_logprobs;
-    a.err = ctx->err;
-    a.stats = ctx->target->verify_ws;
-    a.max_batch = p.max_batch;
-    a.max_rows = p.max_rows;
+    const pld_status st =
+        verify_args(ctx, logits, logits_dtype, logits_stride, rows, draft, draft_len, src,
+                    draft_probs, head, temperature, uniform, batch, out_tokens, out_accepted,
+                    out_counts, out_logprobs, a);
+    if (st != PLD_OK || batch == 0)
+        return st;
     const hipError_t e = pld::launch_verify(a, stream);
     if (e != hipSuccess)
         return hip_fail(e, "verification launch");
+    return PLD_OK;
+}
+
+pld_status pld_kv_append_tree(pld_ctx *ctx, const void *q, int64_t q_stride, const void *k,
+                              const void *v, int64_t kv_stride, int32_t rows,
+                              const int32_t *lengths, const int32_t *draft_len,
+                              const int32_t *parent, int32_t batch, const int32_t *page_table,
+                              int64_t table_stride, void *k_cache, void *v_cache,
+                              int64_t n_pages, const float *k_scale, const float *v_scale,
+                              const float *q_norm, const float *k_norm, float eps, void *out_q,
+                              hipStream_t stream)
+{
+    pld::TreeAppendArgs a;
+    pld_status st =
+        append_args(ctx, q, q_stride, k, v, kv_stride, rows, lengths, draft_len, batch, page_table,
+                    table_stride, k_cache, v_cache, n_pages, k_scale, v_scale, out_q, a.kv);
+    if (st == PLD_OK && parent)
+        st = tree_rows(rows, parent);
+    if (st != PLD_OK)
+        return st;
+    if (((uintptr_t)q_norm | (uintptr_t)k_norm) & 3u)
+        return fail(PLD_EINVAL, "q_norm and k_norm must be 4-byte aligned");
+    if (q_norm && !q && batch > 0)
+        return fail(PLD_EINVAL, "q_norm needs q");
+    if (!(eps >= 0.0f) || !isfinite(eps))
+        return fail(PLD_EINVAL, "eps must be >= 0 and finite");
+    if (batch == 0)
+        return PLD_OK;
+    a.parent = parent;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.eps = eps;
+    const hipError_t e = pld::launch_kv_append_tree(a, stream);
+    if (e != hipSuccess)
+        return hip_fail(e, "cache append launch");
+    return PLD_OK;
+}
+
+pld_status pld_attend_tree(pld_ctx *ctx, const void *q, int64_t q_stride, int32_t rows,
+                           const int32_t *lengths, const int32_t *draft_len,
+                           const int32_t *parent, int64_t max_len, int32_t batch,
+                           const int32_t *page_table, int64_t table_stride, const void *k_cache,
+                           const void *v_cache, int64_t n_pages, const float *k_scale,
+                           const float *v_scale, float scale, int32_t window, void *out,
+                           float *out_lse, hipStream_t stream)
+{
+    pld::AttendArgs a;
+    pld_status st =
+        attend_args(ctx, q, q_stride, rows, lengths, draft_len, max_len, batch, page_table,
+                    table_stride, k_cache, v_cache, n_pages, k_scale, v_scale, scale, window, out,
+                    out_lse, a);
+    if (st == PLD_OK && parent)
+        st = tree_rows(rows, parent);
+    if (st != PLD_OK || batch == 0)
+        return st;
+    a.parent = parent;
+    // (one row is a chain)
+    const hipError_t e = parent && rows > 1 ? pld::launch_attend_tree(a, stream)
+                                            : pld::launch_attend(a, stream);
+    if (e != hipSuccess)
+        return hip_fail(e, "attention launch");
+    return PLD_OK;
+}
+
+pld_status pld_verify_tree(pld_ctx *ctx, const void *logits, int32_t logits_dtype,
+                           int64_t logits_stride, int32_t rows, const int32_t *draft,
+                           const int32_t *draft_len, const int32_t *parent,
+                           const float *temperature, const float *uniform, int32_t batch,
+                           int32_t *out_tokens, int32_t *out_path, int32_t *out_accepted,
+                           int32_t *out_counts, float *out_logprobs, hipStream_t stream)
+{
+    pld::TreeVerifyArgs a;
+    pld_status st =
+        verify_args(ctx, logits, logits_dtype, logits_stride, rows, draft, draft_len, nullptr,
+                    nullptr, 0, temperature, uniform, batch, out_tokens, out_accepted, out_counts,
+                    out_logprobs, a.v);
+    if (st == PLD_OK)
+        st = tree_rows(rows, parent);
+    if (st != PLD_OK)
+        return st;
+    if (batch > 0 && !out_path)
+        return fail(PLD_EINVAL, "null buffer pointer");
+    if ((uintptr_t)out_path & 3u)
+        return fail(PLD_EINVAL, "out_path must be 4-byte aligned");
+    if (batch == 0)
+        return PLD_OK;
+    a.parent = parent;
+    a.out_path = out_path;
+    const hipError_t e = pld::launch_verify_tree(a, stream);
+    if (e != hipSuccess)
+        return hip_fail(e, "verification launch");
+    return PLD_OK;
+}
+
+pld_status pld_kv_keep(pld_ctx *ctx, const int32_t *lengths, const int32_t *draft_len,
+                       const int32_t *path, const int32_t *accepted, int32_t rows, int32_t batch,
+                       const int32_t *page_table, int64_t table_stride, void *k_cache,
+                       void *v_cache, int64_t n_pages, int32_t layers, int64_t k_layer_stride,
+                       int64_t v_layer_stride, hipStream_t stream)
+{
+    pld::KeepArgs a;
+    pld_status st = block_args(ctx, rows, lengths, draft_len, 0, batch, page_table, table_stride,
+                               k_cache, v_cache, n_pages, nullptr, nullptr, a.blk);
+    if (st == PLD_OK)
+        st = tree_rows(rows, nullptr);
+    if (st != PLD_OK)
+        return st;
+    if (batch > 0 && (!path || !accepted))
+        return fail(PLD_EINVAL, "null buffer pointer");
+    if (((uintptr_t)path | (uintptr_t)accepted) & 3u)
+        return fail(PLD_EINVAL, "int32 and float buffers must be 4-byte aligned");
+    if (layers < 0)
+        return fail(PLD_EINVAL, "layers must be >= 0 (got %d)", layers);
+    if (layers > 1) {
+        // (2^31 pages, 2^16 heads, 2^8 positions and dims: below 2^63)
+        const int64_t cells = n_pages * a.blk.kv_heads * ctx->target->p.page_tokens *
+                              (int64_t)a.blk.head_dim;
+        const int64_t word = a.blk.cache_dtype == PLD_E4M3 ? 16 : 8;
+        if (k_layer_stride < cells || v_layer_stride < cells || k_layer_stride % word ||
+            v_layer_stride % word)
+            return fail(PLD_EINVAL, "k_layer_stride and v_layer_stride must hold a layer's cache "
+                        "(%lld elements) and be multiples of 16 bytes", (long long)cells);
+    }
+    if (batch == 0 || layers == 0)
+        return PLD_OK;
+    a.path = path;
+    a.accepted = accepted;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.layers = layers;
+    a.k_layer = layers > 1 ? k_layer_stride : 0;
+    a.v_layer = layers > 1 ? v_layer_stride : 0;
+    const hipError_t e = pld::launch_kv_keep(a, stream);
+    if (e != hipSuccess)
+        return hip_fail(e, "kept cells launch");
     return PLD_OK;
 }
 

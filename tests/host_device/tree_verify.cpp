@@ -1,0 +1,42 @@
+// pld_verify_tree's kernels on the host (see hip/hip_runtime.h): one call, over
+// a workspace that the caller keeps between calls.
+#include <hip/hip_runtime.h>
+
+#define __builtin_amdgcn_readlane(x, i) host_device::from_lane(x, (i) & 63)
+
+#include "pld_tree_verify.hip"
+
+extern "C" {
+
+// order: the wavefronts' order; report: broken barriers, stuck workgroups.
+int host_verify_tree(const pld::TreeVerifyArgs *a, const int32_t *order, int32_t waves,
+                     int64_t *report)
+{
+    host_device::State &s = host_device::state();
+    s.order.assign(order, order + waves);
+    s.broken_barriers = s.stuck = 0;
+    const hipError_t e = pld::launch_verify_tree(*a, nullptr);
+    report[0] = s.broken_barriers;
+    report[1] = s.stuck;
+    return e;
+}
+
+// The launches of a call of these sizes, not run: the threads of the largest
+// grid, or 0 where the sizes are refused.
+uint64_t host_verify_tree_grid(int32_t batch, int32_t rows, int32_t vocab, int32_t dtype)
+{
+    pld::TreeVerifyArgs a;
+    memset(&a, 0, sizeof(a));
+    a.v.dtype = dtype;
+    a.v.rows = a.v.max_rows = rows;
+    a.v.batch = a.v.max_batch = batch;
+    a.v.vocab = vocab;
+    host_device::State &s = host_device::state();
+    s.dry = true;
+    s.most_threads = 0;
+    const hipError_t e = pld::launch_verify_tree(a, nullptr);
+    s.dry = false;
+    return e == hipSuccess ? s.most_threads : 0;
+}
+
+}
