@@ -38,7 +38,8 @@ def sources():
             os.path.join(CSRC, "pld_control.hip"), os.path.join(CSRC, "pld_ngram.hip"),
             os.path.join(CSRC, "pld_kv.hip"), os.path.join(CSRC, "pld_attend.hip"),
             os.path.join(CSRC, "pld_verify.hip"), os.path.join(CSRC, "pld_tree_kv.hip"),
-            os.path.join(CSRC, "pld_tree_attend.hip"), os.path.join(CSRC, "pld_tree_verify.hip"),
+            os.path.join(CSRC, "pld_tree_attend.hip"),
+            os.path.join(CSRC, "pld_tree_attend_f16.hip"), os.path.join(CSRC, "pld_tree_verify.hip"),
             os.path.join(CSRC, "pld_target_api.cpp"),
             os.path.join(CSRC, "pld_api.cpp")]
 

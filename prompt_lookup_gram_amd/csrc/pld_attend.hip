@@ -1,7 +1,7 @@
 // Attention of the verify block's rows over the paged cache, for gfx950
 // (MI355X): the kernels of pld_attend_device.h for blocks that are chains.
 
-#include "pld_attend_device.h"
+#include "pld_attend_launch.h"
 
 namespace pld {
 
@@ -16,6 +16,10 @@ int64_t attend_rows(const pld_target_params &p)
     return spans >= ceil_div(most, rows) ? most : rows * spans;
 }
 
-hipError_t launch_attend(const AttendArgs &a, hipStream_t s) { return launch_blocks<false>(a, s); }
+hipError_t launch_attend(const AttendArgs &a, hipStream_t s)
+{
+    return a.blk.dtype == PLD_BF16 ? launch_blocks<__bf16, false>(a, s)
+                                   : launch_blocks<_Float16, false>(a, s);
+}
 
 }  // namespace pld

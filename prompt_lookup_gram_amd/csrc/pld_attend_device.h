@@ -114,6 +114,7 @@ __device__ __forceinline__ float factor(float c)
 // positions take more than one.
 struct Split {
     int32_t span;
+    int32_t least;     // trees: positions that a span of any request has at least
     int32_t splits;
     int32_t m_tiles;   // tiles of query rows
     float *o;          // [batch][kv_heads][splits][m_tiles * 16 MB][D]
@@ -217,12 +218,27 @@ struct Branches {
     }
 };
 
+// Positions of a request's spans. A tree's are dealt out evenly: a batch with
+// ragged lengths has all of its workgroups at work, each on a share of its own
+// request, where equal spans leave the short requests' idle.
+template <bool TREE, int GRAIN>
+__device__ __forceinline__ int32_t span_of(const Split &sp, const Sight &s)
+{
+    if (!TREE)
+        return sp.span;
+    const int32_t even =
+        (int32_t)(((int64_t)s.hi - s.start) / sp.splits / GRAIN + 1) * GRAIN;
+    return even < sp.least ? sp.least : (even > sp.span ? sp.span : even);
+}
+
 // What both kernels share: MB blocks of 16 query rows a wavefront.
 template <typename T, typename C, int D, int MB, bool TREE>
 struct Tiles {
     static constexpr bool kTree = TREE;
     static constexpr bool kByte = sizeof(C) == 1;
     static constexpr int TK = kByte ? 64 : 32;  // positions of a tile
+    static constexpr int kGrain = kWaves * TK;  // a span is a multiple of so many positions
+    static constexpr int64_t kSpanBytes = 4 << 20;
     static constexpr int NB = TK / 32;          // 32-position steps of V^T P^T
     static constexpr int CH = 8 * NB;           // positions of a lane's V word
     static constexpr int DB = D / 16;           // blocks of 16 dims
@@ -557,13 +573,14 @@ __device__ __forceinline__ bool work_of(const AttendArgs &a, const Split &sp, Wo
         return false;
     w.m1 = w.m0 + M < n * w.G ? w.m0 + M : n * w.G;
     const Sight s = sight_of<K::TK, K::kTree>(a, w.length, w.m0 / w.G, (w.m1 - 1) / w.G);
-    const int64_t s0 = s.start + (int64_t)split * sp.span;
+    const int32_t span = span_of<K::kTree, K::kGrain>(sp, s);
+    const int64_t s0 = s.start + (int64_t)split * span;
     if (s0 > s.hi)
         return false;
     w.s0 = (int32_t)s0;
-    w.s1 = sp.span <= s.hi - w.s0 ? w.s0 + sp.span - 1 : s.hi;
+    w.s1 = span <= s.hi - w.s0 ? w.s0 + span - 1 : s.hi;
     w.lo = s.lo;
-    w.whole = sp.span > s.hi - s.start;
+    w.whole = span > s.hi - s.start;
     w.at = (((int64_t)w.b * g.kv_heads + w.h) * sp.splits + split) * (sp.m_tiles * (int64_t)M);
     return true;
 }
@@ -1043,7 +1060,7 @@ __global__ __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) void attend_wide(A
 // lane takes 4 dims of every 256 / D'th span (D' = D up to a power of two);
 // 8 loads are in flight, since a span's partial results are a round trip to
 // L2 away and the launch is short.
-template <typename T, int D, int TK, int M, bool TREE>
+template <typename T, int D, int TK, int M, bool TREE, int GRAIN>
 __global__ __launch_bounds__(kWave) void join_kernel(AttendArgs a, Split sp)
 {
     constexpr int kLanes = D <= 64 ? 16 : (D <= 128 ? 32 : 64);  // of a span
@@ -1062,7 +1079,7 @@ __global__ __launch_bounds__(kWave) void join_kernel(AttendArgs a, Split sp)
     const int32_t row = t * G + hd - h * G, m0 = row / M * M;
     const int32_t m1 = m0 + M < n * G ? m0 + M : n * G;
     const Sight s = sight_of<TK, TREE>(a, length, m0 / G, (m1 - 1) / G);
-    const int32_t spans = (s.hi - s.start) / sp.span + 1;
+    const int32_t spans = (s.hi - s.start) / span_of<TREE, GRAIN>(sp, s) + 1;
     if (spans == 1)
         return;
     const int64_t rows = (int64_t)sp.m_tiles * M;
@@ -1112,107 +1129,6 @@ __global__ __launch_bounds__(kWave) void join_kernel(AttendArgs a, Split sp)
             U2{pack2<T>(y[0] / sum, y[1] / sum), pack2<T>(y[2] / sum, y[3] / sum)};
     if (a.out_lse && lane == 0)
         a.out_lse[r] = (top - kLift) * kLn2 + __logf(sum);
-}
-
-// Positions of a span. A workgroup streams about 14 KB a microsecond (two on
-// each compute unit share what HBM gives) and takes some 10 us to start and
-// to join, so a span should hold kSpanBytes of cache, as long as kEvenGroups
-// workgroups can be had; never more than it takes for kMostGroups of them
-// (ragged requests even out). A small batch is cut further to fill the chip,
-// down to 32 positions a query row: the partial results are 8 bytes a dim,
-// written and read, against 4 of cache. 16 x 262,144 positions, 128 rows:
-// 985 us with 2 MiB, 918 with 4 MiB; 32 x 16,384, 64 rows: 294 us with 64
-// positions a row, 236 with 32.
-constexpr int64_t kFillGroups = 512;
-constexpr int64_t kEvenGroups = 1024;
-constexpr int64_t kMostGroups = 4096;
-constexpr int64_t kSpanBytes = 4 << 20;
-constexpr int32_t kMinSpan = 256;
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Lays out a launch of kernel K and starts it, then the join.
-template <typename K, typename T, int D, typename F>
-hipError_t launch_split(const AttendArgs &a, F kernel, hipStream_t s)
-{
-    const BlockArgs &g = a.blk;
-    const int64_t m = (int64_t)g.rows * (g.q_heads / g.kv_heads);
-    Split sp;
-    sp.m_tiles = (int32_t)((m + K::M - 1) / K::M);
-    const int64_t sight = a.window && (int64_t)a.window + g.rows - 1 + K::TK < g.max_len
-                              ? (int64_t)a.window + g.rows - 1 + K::TK
-                              : g.max_len;
-    const int64_t groups = (int64_t)g.batch * g.kv_heads * sp.m_tiles;
-    const int64_t tile = kWaves * K::TK, used = std::min<int64_t>(K::M, m);
-    const int64_t total = sight * groups, bytes = 2 * D * K::kCellBytes;
-    int64_t span = std::min<int64_t>(ceil_div(total, kFillGroups), 32 * used);
-    span = std::max(span, std::min(ceil_div(total, kEvenGroups), kSpanBytes / bytes));
-    span = std::max({span, ceil_div(total, kMostGroups), (int64_t)kMinSpan});
-    // the workspace holds the partial results of so many spans
-    const int64_t room = a.ws_rows / (groups * K::M);
-    span = std::max(span, room < 2 ? sight : ceil_div(sight, room));
-    span = ceil_div(span, tile) * tile;
-    const int64_t splits = ceil_div(sight, span);
-    sp.span = span < 0x7fffffffLL ? (int32_t)span : 0x7fffffff;
-    sp.splits = (int32_t)splits;
-    sp.o = a.ws;
-    sp.ml = (float2 *)(a.ws + a.ws_rows * D);
-    const int64_t chunks = ceil_div((int64_t)g.batch * g.kv_heads * splits, 8) * 8;
-    const int64_t joins = (int64_t)g.batch * g.rows * g.q_heads;
-    if (!fits_grid(chunks * sp.m_tiles, kWaves * kWave) ||
-        (splits > 1 && !fits_grid(joins, kWave)))
-        return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)(chunks * sp.m_tiles)), dim3(kWaves * kWave), 0, s,
-                       a, sp);
-    if (splits > 1)
-        hipLaunchKernelGGL((join_kernel<T, D, K::TK, K::M, K::kTree>), dim3((uint32_t)joins), dim3(kWave),
-                           0, s, a, sp);
-    return hipGetLastError();
-}
-
-// The kernel by the query rows of a kv head. Measured with 16-bit cells, 16
-// requests of 65,536 positions and 2 kv heads, in us: narrow with 16 and 32 rows
-// a workgroup, wide with 64 and 128. head_dim 128: 16 rows 202, 205, 207, 225; 17
-// rows 277, 206, 208, 228; 32 rows 280, 212, 214, 234; 33 rows 416, 280, 217, 234;
-// 64 rows 479, 285, 230, 248; 65 rows 650, 418, 320, 248. head_dim 256 (no narrow
-// with 32): 16 rows 386, 546, 588; 17 rows 560, 548, 597; 64 rows 1,036, 573, 621;
-// 65 rows 1,268, 944, 621. 8-bit cells take the same rule; there narrow with 32
-// would hold out longer (head_dim 128, 64 rows: 144 against 168).
-template <typename T, typename C, int D, bool TREE>
-hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
-{
-    const int64_t m = (int64_t)a.blk.rows * (a.blk.q_heads / a.blk.kv_heads);
-    if (m <= 16)
-        return launch_split<Narrow<T, C, D, 1, TREE>, T, D>(a, attend_narrow<T, C, D, 1, TREE>, s);
-    if constexpr (D <= 128)
-        if (m <= 32)
-            return launch_split<Narrow<T, C, D, 2, TREE>, T, D>(a, attend_narrow<T, C, D, 2, TREE>, s);
-    if (m <= 64)
-        return launch_split<Wide<T, C, D, 1, TREE>, T, D>(a, attend_wide<T, C, D, 1, TREE>, s);
-    return launch_split<Wide<T, C, D, 2, TREE>, T, D>(a, attend_wide<T, C, D, 2, TREE>, s);
-}
-
-template <typename T, typename C, bool TREE>
-hipError_t launch_typed(const AttendArgs &a, hipStream_t s)
-{
-    switch (a.blk.head_dim) {
-    case 64: return launch_dim<T, C, 64, TREE>(a, s);
-    case 96: return launch_dim<T, C, 96, TREE>(a, s);
-    case 128: return launch_dim<T, C, 128, TREE>(a, s);
-    case 192: return launch_dim<T, C, 192, TREE>(a, s);
-    default: return launch_dim<T, C, 256, TREE>(a, s);
-    }
-}
-
-template <bool TREE>
-hipError_t launch_blocks(const AttendArgs &a, hipStream_t s)
-{
-    const bool wide = a.blk.cache_dtype != PLD_E4M3;
-    if (a.blk.dtype == PLD_BF16)
-        return wide ? launch_typed<__bf16, __bf16, TREE>(a, s)
-                    : launch_typed<__bf16, E4m3, TREE>(a, s);
-    return wide ? launch_typed<_Float16, _Float16, TREE>(a, s)
-                : launch_typed<_Float16, E4m3, TREE>(a, s);
 }
 
 }  // namespace

@@ -134,6 +134,7 @@ hipError_t launch_attend(const AttendArgs &a, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t s);
 hipError_t launch_kv_append_tree(const TreeAppendArgs &a, hipStream_t s);
 hipError_t launch_attend_tree(const AttendArgs &a, hipStream_t s);
+hipError_t launch_attend_tree_f16(const AttendArgs &a, hipStream_t s);
 hipError_t launch_verify_tree(const TreeVerifyArgs &a, hipStream_t s);
 hipError_t launch_kv_keep(const KeepArgs &a, hipStream_t s);
 
