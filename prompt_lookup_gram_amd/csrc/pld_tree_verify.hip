@@ -15,18 +15,16 @@
 //  - all rows at once (rows_kernel), a piece of a row a workgroup; the
 //    workgroup that completes a row decides which child it leads to, and the
 //    path is a walk over these decisions. One round trip, however deep;
-//  - the path alone (walk_kernel), one workgroup a request, a row after the
-//    other: nothing is read that is not needed.
+//  - the path alone (walk_kernel), a row after the other by a team of workgroups a
+//    request: nothing is read that is not needed.
 // The row that the walk ends at is then read once more, in 64 bits, for the
 // draw (draw_kernel), as in pld_verify.hip.
 //
 // Decisions are made in 64 bits from a 32-bit sum Z of the weights, whose
-// relative error is below 48 * 2^-23: pld_verify.hip derives it for the pieces;
-// on the path a thread's arguments reach 8 above its base, which adds 8.3 *
-// 2^-23, but only 11 additions in a row are in 32 bits, 5.5 * 2^-23 where the
-// pieces have 20. R carries the error of Z as it is, so a decision within 2^-17
-// u Z of its edge is made again from a sum with 64-bit arguments, and within
-// 2^-22 from one with 64-bit exponentials.
+// relative error is below 48 * 2^-23 (pld_verify.hip derives it). R carries the
+// error of Z as it is, so a decision within 2^-17 u Z of its edge is made again
+// from a sum with 64-bit arguments, and within 2^-22 from one with 64-bit
+// exponentials.
 
 #include <hip/hip_runtime.h>
 #include <float.h>
@@ -179,35 +177,33 @@ __device__ __forceinline__ void child_logits(const Draft &d, const T *z, int32_t
         zx[i] = d.up[i] == v ? to_f32(z[d.token[i]]) : 0.0f;
 }
 
-// All rows at once: one workgroup per piece of a row, W 16-byte words a thread.
-template <typename T, int W>
-__global__ __launch_bounds__(kThreads) void rows_kernel(TreeVerifyArgs ta, Space sp,
-                                                        uint32_t pieces)
-{
-    const VerifyArgs &a = ta.v;
-    constexpr int N = 16 / sizeof(T);
-    constexpr int kPiece = W * N * kThreads;
-    __shared__ float lds_max[kWaves], lds_sum[kWaves];
-    __shared__ int32_t lds_arg[kWaves];
-    const int32_t piece = blockIdx.x % pieces, tid = threadIdx.x;
-    const uint32_t order = blockIdx.x / pieces;
-    const int32_t b = order % (uint32_t)a.batch, t = order / (uint32_t)a.batch;
-    const int wave = tid / kWave, lane = tid % kWave;
-    const int32_t n = nodes_of(a, b);
-    if (t >= n)
-        return;
-    const T *z = (const T *)a.logits + ((int64_t)b * a.rows + t) * a.stride;
-    const float tf = temperature(a, b);
-    const bool greedy = tf == 0.0f;
-    const float c = kLog2e / (greedy ? 1.0f : tf);
+// What a workgroup finds in a piece of a row: on thread 0.
+struct Found {
+    float top, sum;
+    int32_t arg;
+};
+struct Scratch {
+    float top[kWaves], sum[kWaves];
+    int32_t arg[kWaves];
+};
 
+// The largest logit of a piece, where it is (greedy) and the sum of the
+// weights, W 16-byte words a thread, in one read. Every wavefront but the first
+// may go on when it returns; s is free again after the next barrier.
+template <typename T, int W>
+__device__ __forceinline__ Found search(const T *z, int32_t vocab, int32_t piece, float c,
+                                        bool greedy, Scratch &s)
+{
+    constexpr int N = 16 / sizeof(T);
+    const int32_t tid = threadIdx.x;
+    const int wave = tid / kWave, lane = tid % kWave;
     float x[W * N];
     float top = -INFINITY;
-    const int32_t lo = piece * kPiece + tid * N;
+    const int32_t lo = piece * (W * N * kThreads) + tid * N;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const int32_t i = lo + w * (kThreads * N);
-        if (i <= a.vocab - N) {
+        if (i <= vocab - N) {
             const Word<T> y = *(const Word<T> *)(z + i);
 #pragma unroll
             for (int k = 0; k < N; ++k)
@@ -215,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(TreeVerifyArgs ta, Space
         } else {
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                x[w * N + k] = i + k < a.vocab ? to_f32(z[i + k]) : -INFINITY;
+                x[w * N + k] = i + k < vocab ? to_f32(z[i + k]) : -INFINITY;
         }
     }
 #pragma unroll
@@ -223,12 +219,12 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(TreeVerifyArgs ta, Space
         top = fmaxf(top, x[k]);
     top = wave_max(top);
     if (lane == 0)
-        lds_max[wave] = top;
+        s.top[wave] = top;
     __syncthreads();
-    top = lds_max[0];
+    top = s.top[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w)
-        top = fmaxf(top, lds_max[w]);
+        top = fmaxf(top, s.top[w]);
     // (as in pld_verify.hip: one operation a logit, what rounding takes off the
     // common exponent put back into the sum, or two where logits are far)
     float base = top * c, rest = 0.0f, sum = 0.0f;
@@ -256,37 +252,42 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(TreeVerifyArgs ta, Space
         }
     }
     if (lane == 0) {
-        lds_sum[wave] = sum;
-        lds_arg[wave] = arg;
+        s.sum[wave] = sum;
+        s.arg[wave] = arg;
     }
     __syncthreads();
-    if (wave > 0)
-        return;  // one wavefront counts the piece in, and decides if it is the last
-    const int64_t r = (int64_t)b * a.rows + t;
-    Piece *const mine = sp.pieces + r * pieces;
-    int32_t count = 0;
-    if (lane == 0) {
+    if (tid == 0) {
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) {
-            sum += lds_sum[w];
-            arg = lds_arg[w] < arg ? lds_arg[w] : arg;
+            sum += s.sum[w];
+            arg = s.arg[w] < arg ? s.arg[w] : arg;
         }
         sum *= __builtin_amdgcn_exp2f(-rest);
-        poke(&mine[piece].top_sum,
-             (unsigned long long)__float_as_uint(top) << 32 | __float_as_uint(sum));
-        if (greedy)
-            poke(&mine[piece].arg, (unsigned long long)(uint32_t)arg);
-        count = arrive(sp.arrived + r);
     }
-    if (__builtin_amdgcn_readfirstlane(count) != (int32_t)pieces - 1)
-        return;
+    return Found{top, sum, arg};
+}
 
-    // this wavefront completes the row: join the pieces and decide
-    Draft d;
-    (void)d.load(ta, b, n, greedy, lane);
-    float zx[kParts];
-    child_logits(d, z, t, zx);
+// A piece's findings, for the workgroup that joins the row; one thread. Its
+// stores are complete when it counts itself in.
+__device__ __forceinline__ void leave(Piece *at, const Found &f, bool greedy)
+{
+    poke(&at->top_sum, (unsigned long long)__float_as_uint(f.top) << 32 | __float_as_uint(f.sum));
+    if (greedy)
+        poke(&at->arg, (unsigned long long)(uint32_t)f.arg);
+}
+
+// Joins the pieces of node t's row and decides which child it leads to; one
+// wavefront, the same on every lane.
+template <typename T>
+__device__ __forceinline__ int32_t decide(const VerifyArgs &a, const Space &sp, const Draft &d,
+                                          int32_t b, int32_t t, const T *z,
+                                          const float (&zx)[kParts], uint32_t pieces, float tf,
+                                          int lane)
+{
+    const bool greedy = tf == 0.0f;
     const double inv = greedy ? 1.0 : 1.0 / (double)tf;
+    const int64_t r = (int64_t)b * a.rows + t;
+    const Piece *const mine = sp.pieces + r * pieces;
     float m = -INFINITY;
     for (uint32_t i = lane; i < pieces; i += kWave)
         m = fmaxf(m, __uint_as_float((uint32_t)(peek(&mine[i].top_sum) >> 32)));
@@ -314,129 +315,121 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(TreeVerifyArgs ta, Space
         next = child_of(d, z, a.vocab, t, zx, m, total, inv, greedy, best, lane);
     if (lane == 0)
         ((Node *)sp.rows)[r] = Node{total, m, best, next, {0, 0, 0}};
+    return next;
 }
 
-constexpr int kWalkers = 1024;  // threads of a walk
-
-// The path alone: one workgroup a request, a row after the other.
-template <typename T>
-__global__ __launch_bounds__(kWalkers) void walk_kernel(TreeVerifyArgs ta, Space sp)
+// All rows at once: one workgroup per piece of a row.
+template <typename T, int W>
+__global__ __launch_bounds__(kThreads) void rows_kernel(TreeVerifyArgs ta, Space sp,
+                                                        uint32_t pieces)
 {
     const VerifyArgs &a = ta.v;
-    constexpr int N = 16 / sizeof(T), kDeep = 32 / N, kLong = kWalkers / kWave;
-    __shared__ float lds_top[kLong];
-    __shared__ double lds_sum[kLong];
-    __shared__ int32_t lds_arg[kLong], lds_next;
-    const int32_t b = blockIdx.x, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    __shared__ Scratch lds;
+    const int32_t piece = blockIdx.x % pieces, lane = threadIdx.x % kWave;
+    const uint32_t order = blockIdx.x / pieces;
+    const int32_t b = order % (uint32_t)a.batch, t = order / (uint32_t)a.batch;
+    const int32_t n = nodes_of(a, b);
+    if (t >= n)
+        return;
+    const int64_t r = (int64_t)b * a.rows + t;
+    const T *z = (const T *)a.logits + r * a.stride;
+    const float tf = temperature(a, b);
+    const bool greedy = tf == 0.0f;
+    const Found f =
+        search<T, W>(z, a.vocab, piece, kLog2e / (greedy ? 1.0f : tf), greedy, lds);
+    if (threadIdx.x >= kWave)
+        return;  // one wavefront counts the piece in, and decides if it is the last
+    int32_t count = 0;
+    if (lane == 0) {
+        leave(sp.pieces + r * pieces + piece, f, greedy);
+        count = arrive(sp.arrived + r);
+    }
+    if (__builtin_amdgcn_readfirstlane(count) != (int32_t)pieces - 1)
+        return;
+    Draft d;
+    (void)d.load(ta, b, n, greedy, lane);
+    float zx[kParts];
+    child_logits(d, z, t, zx);
+    (void)decide(a, sp, d, b, t, z, zx, pieces, tf, lane);
+}
+
+constexpr int32_t kThere = -1;     // `stop` once a walk has ended
+constexpr int32_t kDone = 1 << 16;  // `arrived` counts pieces taken below, pieces done above
+
+// The path alone: a team of workgroups a request. They take the pieces of the
+// walk's row one by one; who completes the row decides where the walk goes on,
+// and says so in `stop`. A workgroup that finds every piece of the row taken
+// waits for that. It waits for workgroups that run and wait for nothing
+// themselves while they have a piece: the walk ends however many of a team the
+// chip has room for, one included.
+template <typename T, int W>
+__global__ __launch_bounds__(kThreads) void walk_kernel(TreeVerifyArgs ta, Space sp,
+                                                        uint32_t pieces, uint32_t team)
+{
+    const VerifyArgs &a = ta.v;
+    __shared__ Scratch lds;
+    __shared__ int32_t lds_piece, lds_node;
+    const int32_t b = blockIdx.x / team, tid = threadIdx.x, lane = tid % kWave;
+    const bool first = tid < kWave;
     const int32_t n = nodes_of(a, b);
     if (n <= 0)
         return;
     const float tf = temperature(a, b);
     const bool greedy = tf == 0.0f;
     const float c = kLog2e / (greedy ? 1.0f : tf);
-    const double inv = greedy ? 1.0 : 1.0 / (double)tf;
     Draft d;
     if (d.load(ta, b, n, greedy, lane))
         return;  // (the draw finds the same)
+    int32_t *const stop = sp.stop + b;
     int32_t node = 0;
     for (;;) {
-        const T *z = (const T *)a.logits + ((int64_t)b * a.rows + node) * a.stride;
+        const int64_t r = (int64_t)b * a.rows + node;
+        if (tid == 0)
+            lds_piece = __hip_atomic_fetch_add(sp.arrived + r, 1, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT) & (kDone - 1);
+        __syncthreads();
+        const int32_t piece = lds_piece;
+        if (piece >= (int32_t)pieces) {
+            if (tid == 0) {
+                int32_t to = peek(stop);
+                while (to == (node ? node : kNever)) {
+                    __builtin_amdgcn_s_sleep(2);
+                    to = peek(stop);
+                }
+                lds_node = to;
+            }
+            __syncthreads();
+            node = lds_node;
+            if (node == kThere)
+                return;
+            continue;
+        }
+        const T *z = (const T *)a.logits + r * a.stride;
         float zx[kParts];
-        if (wave == 0)
+        if (first)
             child_logits(d, z, node, zx);
-        // this thread's largest logit, where it is, and the sum of 2^(c (z -
-        // base)): a round of kDeep words is added up in 32 bits, rounds in 64;
-        // the base follows the largest logit once that is far above it
-        float top = -INFINITY, base = -INFINITY;
-        int32_t arg = 0x7fffffff;
-        double sum = 0.0;
-        for (int32_t from = tid * N; from < a.vocab; from += kWalkers * N * kDeep) {
-            float x[kDeep * N];
-#pragma unroll
-            for (int w = 0; w < kDeep; ++w) {
-                const int32_t i = from + w * (kWalkers * N);
-                if (i <= a.vocab - N) {
-                    const Word<T> y = *(const Word<T> *)(z + i);
-#pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        x[w * N + k] = to_f32(y.x[k]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        x[w * N + k] = i + k < a.vocab ? to_f32(z[i + k]) : -INFINITY;
-                }
-            }
-            float high = x[0];
-#pragma unroll
-            for (int k = 1; k < kDeep * N; ++k)
-                high = fmaxf(high, x[k]);
-            if (high > top) {
-                top = high;
-                if (greedy) {
-#pragma unroll
-                    for (int k = kDeep * N - 1; k >= 0; --k)
-                        if (x[k] == top)
-                            arg = from + k / N * (kWalkers * N) + k % N;
-                }
-                if (!((top - base) * c < 8.0f)) {
-                    sum *= base == -INFINITY ? 0.0 : exp(((double)base - top) * inv);
-                    base = top;
-                }
-            }
-            const float zero = base == -INFINITY ? 0.0f : base;
-            float part[N];
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                part[k] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kDeep * N; ++k)
-                part[k % N] += __builtin_amdgcn_exp2f((x[k] - zero) * c);
-#pragma unroll
-            for (int k = 1; k < N; ++k)
-                part[0] += part[k];
-            sum += (double)part[0];
-        }
-        // join the threads
-        const float high = wave_max(top);
-        if (greedy) {
-            arg = top == high ? arg : 0x7fffffff;
-            for (int i = kWave / 2; i; i >>= 1) {
-                const int32_t y = __shfl_xor(arg, i);
-                arg = y < arg ? y : arg;
-            }
-        }
-        const double part = wave_sum(base == -INFINITY ? sum : sum * exp(((double)base - high) * inv));
-        if (lane == 0) {
-            lds_top[wave] = high;
-            lds_sum[wave] = part;
-            lds_arg[wave] = arg;
-        }
-        __syncthreads();
-        if (wave == 0) {
-            const bool in = lane < kLong;
-            const float mine = in ? lds_top[lane] : -INFINITY;
-            const float m = wave_max(mine);
-            double total = in ? lds_sum[lane] : 0.0;
-            total = wave_sum(mine == -INFINITY ? total : total * exp(((double)mine - m) * inv));
-            int32_t best = in && mine == m ? lds_arg[lane] : 0x7fffffff;
-            for (int i = kWave / 2; i; i >>= 1) {
-                const int32_t y = __shfl_xor(best, i);
-                best = y < best ? y : best;
-            }
-            int32_t next = -1;
-            if (total > 0.0 && m < INFINITY)
-                next = child_of(d, z, a.vocab, node, zx, m, total, inv, greedy, best, lane);
+        const Found f = search<T, W>(z, a.vocab, piece, c, greedy, lds);
+        if (first) {
+            int32_t count = 0, next = node;
             if (lane == 0) {
-                ((Node *)sp.rows)[(int64_t)b * a.rows + node] =
-                    Node{total, m, best, next, {0, 0, 0}};
-                lds_next = next;
+                leave(sp.pieces + r * pieces + piece, f, greedy);
+                asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+                count = __hip_atomic_fetch_add(sp.arrived + r, kDone, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT) / kDone;
             }
+            if (__builtin_amdgcn_readfirstlane(count) == (int32_t)pieces - 1) {
+                next = decide(a, sp, d, b, node, z, zx, pieces, tf, lane);
+                next = next > 0 ? next : kThere;
+                if (lane == 0)
+                    poke(stop, next);
+            }
+            if (lane == 0)
+                lds_node = next;
         }
         __syncthreads();
-        node = lds_next;
-        if (node <= 0)
+        node = lds_node;
+        if (node == kThere)
             return;
-        // (lds_next is written again only after the next barrier)
     }
 }
 
@@ -519,6 +512,7 @@ __device__ __forceinline__ void finish(const TreeVerifyArgs &ta, const Space &sp
     if (first == 0) {
         a.out_accepted[b] = p.none ? 0 : p.steps;
         a.out_counts[b] = p.none ? 0 : p.steps + 1;
+        sp.stop[b] = kNever;
         sp.drawn[b] = 0;
         if (p.bad)
             atomicOr(a.err, (uint32_t)kErrBlock);
@@ -746,7 +740,22 @@ hipError_t launch_draw(const TreeVerifyArgs &a, const Space &sp, hipStream_t s)
     return start(draw_kernel<T, E>, kThreads, a.v.batch * groups, s, a, sp, (int32_t)groups);
 }
 
-constexpr int64_t kAllBytes = 24 << 20;  // of logits, up to which all rows are read
+// Bytes of logits (of the padded rows) up to which all rows are read. Measured
+// with ragged trees, all rows and the path, the call: 1 tree of 64 rows of 151,936
+// bf16 logits 22 us (the same call), 4 trees 28 and 42, 8 (155 MB) 50 and 51, 16 (311
+// MB) 70 and 71, 24 80 and 61, 64 239 and 87; 64 of 16 rows (311 MB) 77 and 97; 64 of 32
+// rows of 50,257 (206 MB) 62 and 64; 16 full ones of those (51 MB, greedy) 27 and 62.
+constexpr int64_t kAllBytes = 256 << 20;
+constexpr int64_t kResident = 2048;      // workgroups of a walk that the chip holds at once
+
+template <typename T, int W>
+hipError_t launch_walk(const TreeVerifyArgs &a, const Space &sp, int64_t pieces, hipStream_t s)
+{
+    const int64_t room = kResident / a.v.batch;
+    const int64_t team = pieces < room ? pieces : (room > 1 ? room : 1);
+    return start(walk_kernel<T, W>, kThreads, a.v.batch * team, s, a, sp, (uint32_t)pieces,
+                 (uint32_t)team);
+}
 
 template <typename T>
 hipError_t launch_typed(const TreeVerifyArgs &a, hipStream_t s)
@@ -758,7 +767,7 @@ hipError_t launch_typed(const TreeVerifyArgs &a, hipStream_t s)
     const int64_t small = pieces_of(v.vocab, kMinPiece);
     hipError_t e;
     if (rows * v.vocab * (int64_t)sizeof(T) > kAllBytes)
-        e = start(walk_kernel<T>, kWalkers, v.batch, s, a, sp);
+        e = launch_walk<T, kWide>(a, sp, wide, s);
     else if (wide * rows >= kManyPieces && v.vocab > kMinPiece)
         e = start(rows_kernel<T, kWide>, kThreads, rows * wide, s, a, sp, (uint32_t)wide);
     else

@@ -3,19 +3,40 @@
 #include <hip/hip_runtime.h>
 
 #define __builtin_amdgcn_readlane(x, i) host_device::from_lane(x, (i) & 63)
+// (a workgroup runs alone: what it would wait for must not be left to others)
+#define __builtin_amdgcn_s_sleep(n) abort()
 
 #include "pld_tree_verify.hip"
 
 extern "C" {
 
-// order: the wavefronts' order; report: broken barriers, stuck workgroups.
+// order: the wavefronts' order; report: broken barriers, stuck workgroups. walk:
+// only the rows on the path are read, whatever the sizes, in pieces of 2,048
+// logits.
 int host_verify_tree(const pld::TreeVerifyArgs *a, const int32_t *order, int32_t waves,
-                     int64_t *report)
+                     int32_t walk, int64_t *report)
 {
     host_device::State &s = host_device::state();
     s.order.assign(order, order + waves);
     s.broken_barriers = s.stuck = 0;
-    const hipError_t e = pld::launch_verify_tree(*a, nullptr);
+    hipError_t e;
+    if (walk) {
+        const pld::VerifyArgs &v = a->v;
+        const pld::Space sp =
+            pld::space_of((char *)v.stats, v.max_batch, v.max_rows, v.vocab, nullptr);
+        const int64_t pieces = pld::pieces_of(v.vocab, pld::kMinPiece);
+        const auto both = [&](auto x, auto words) {
+            typedef decltype(x) T;
+            const hipError_t w = pld::launch_walk<T, words.value>(*a, sp, pieces, nullptr);
+            return w != hipSuccess ? w : pld::launch_draw<T, 8>(*a, sp, nullptr);
+        };
+        e = v.dtype == PLD_F32
+                ? both(0.0f, std::integral_constant<int, 2>())
+                : (v.dtype == PLD_F16 ? both((_Float16)0, std::integral_constant<int, 1>())
+                                      : both((__bf16)0, std::integral_constant<int, 1>()));
+    } else {
+        e = pld::launch_verify_tree(*a, nullptr);
+    }
     report[0] = s.broken_barriers;
     report[1] = s.stuck;
     return e;

@@ -42,7 +42,7 @@ def build(folder, source):
                     os.path.join(H.HERE, "host_device", source), "-o", lib], check=True)
     out = ctypes.CDLL(lib)
     if source == "tree_verify.cpp":
-        out.host_verify_tree.argtypes = [ctypes.POINTER(VerifyArgs), vp, i32, vp]
+        out.host_verify_tree.argtypes = [ctypes.POINTER(VerifyArgs), vp, i32, i32, vp]
         out.host_verify_tree_grid.restype = ctypes.c_uint64
         out.host_verify_tree_grid.argtypes = [i32] * 4
     else:
@@ -52,9 +52,10 @@ def build(folder, source):
 
 
 def verify(lib, ctx, logits, dtype, draft, dlen, parent, uniform, temperature=None,
-           order=H.ORDERS[0]):
+           order=H.ORDERS[0], walk=False):
     """One call on a host_verify.Context: (tokens, path, accepted, counts,
-    logprobs, error bits, broken barriers)."""
+    logprobs, error bits, broken barriers). walk: only the path's rows are
+    read."""
     b, rows, v = logits.shape
     keep = [np.ascontiguousarray(x) if x is not None else None for x in (
         logits, np.asarray(draft, np.int32), np.asarray(dlen, np.int32),
@@ -70,7 +71,8 @@ def verify(lib, ctx, logits, dtype, draft, dlen, parent, uniform, temperature=No
                           logp.ctypes.data, err.ctypes.data, ctx.ptr, *ctx.size[:2]),
                    ptr[5], path.ctypes.data)
     o, report = np.asarray(order, np.int32), np.zeros(2, np.int64)
-    assert lib.host_verify_tree(ctypes.byref(a), o.ctypes.data, len(o), report.ctypes.data) == 0
+    assert lib.host_verify_tree(ctypes.byref(a), o.ctypes.data, len(o), int(walk),
+                                report.ctypes.data) == 0
     assert report[1] == 0, "a workgroup waits for ever"
     assert (ctx.raw[:ctx.at] == 0xa5).all() and (
         ctx.raw[ctx.at + ctx.bytes:] == 0xa5).all(), "outside the workspace"

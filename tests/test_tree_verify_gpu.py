@@ -1,10 +1,8 @@
 """pld_verify_tree (HIP, gfx950) against the 64-bit reference: tokens, paths and
 counts equal, log probabilities within their bound.
 
-Tolerances are those of tests/test_verify_gpu.py: 2^-17 + 2^-23 |ln p| (the
-sum of a row read along the path is as good as that of one read in pieces:
-arguments reach 8 above a thread's base, 8.3 * 2^-23 more, and 11 additions in a
-row stand for 40, 14 * 2^-23 less). Tokens and paths are compared exactly: the
+Tolerances are those of tests/test_verify_gpu.py: 2^-17 + 2^-23 |ln p|, rows
+being summed in the same pieces. Tokens and paths are compared exactly: the
 inputs' random numbers lie off the edges by far more than 64-bit rounding."""
 
 from __future__ import annotations
@@ -17,6 +15,16 @@ from prompt_lookup_gram_amd import binding as B
 from test_verify_gpu import context, gpu, torch_type  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+class Rows:
+    """A request's logits: the reference looks at the rows on the path."""
+
+    def __init__(self, rows):
+        self.rows = rows
+
+    def __getitem__(self, t):
+        return self.rows[t].double().cpu().numpy()
 
 
 class Case:
@@ -76,7 +84,7 @@ class Case:
 
     def compare(self, out, skip=()):
         tok, path, acc, cnt, logp = [x.cpu().numpy() for x in out]
-        z = self.logits.double().cpu().numpy()[..., :self.vocab]
+        z = [Rows(x[:, :self.vocab]) for x in self.logits]
         for b in range(self.batch):
             if b in skip or self.dlen[b] < 0:
                 assert (tok[b] == -1).all() and (path[b] == -1).all() and (logp[b] == 0).all()
@@ -90,6 +98,125 @@ class Case:
             assert acc[b] == n - 1 and cnt[b] == n
             assert (np.abs(logp[b, :n] - lp) <= 2.0**-17 + 2.0**-23 * np.abs(lp)).all()
             assert (logp[b, n:] == 0).all()
+
+
+class Large(Case):
+    """More than 256 MiB of logits, made on the GPU: only rows on the path are
+    read."""
+
+    def __init__(self, batch, rows, vocab, dt="f32", seed=0, temperature=1.0, accept=0.8, dlen=None,
+                 kind=None, pad=0, offset=0):
+        import torch
+        rng = np.random.default_rng([9823, seed])
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.batch, self.rows, self.vocab, self.dt = batch, rows, vocab, dt
+        d, self.stride = rows - 1, vocab + pad
+        self.parent = np.array([TR.shapes(d)[kind] if kind else TR.random_tree(rng, d)
+                                for _ in range(batch)], np.int32)
+        self.draft = rng.integers(0, vocab, (batch, d)).astype(np.int32)
+        self.temp = np.broadcast_to(np.asarray(temperature, np.float32), (batch,)).copy()
+        self.raw = torch.full((batch * rows * self.stride + offset,), float("nan"),
+                              dtype=torch_type(dt), device="cuda")
+        assert self.raw.nbytes > 256 << 20
+        self.logits = self.raw[offset:].view(batch, rows, self.stride)
+        for b in range(batch):
+            z = torch.randn((rows, vocab), generator=gen, device="cuda") * 2
+            scale = float(self.temp[b]) or 1.0
+            parent = torch.from_numpy(self.parent[b]).long().cuda()
+            x = torch.from_numpy(self.draft[b]).long().cuda()
+            kids = torch.bincount(parent, minlength=rows)[parent]
+            share = accept * torch.rand(d, generator=gen, device="cuda") / kids
+            z[parent, x] = scale * (torch.logsumexp(z / scale, 1)[parent] + torch.logit(share))
+            if self.temp[b] == 0:
+                hit = torch.rand(d, generator=gen, device="cuda") < accept / kids
+                z[parent[hit], x[hit]] = z.amax(1)[parent[hit]] + 1
+            self.logits[b, :, :vocab] = z.to(self.raw.dtype)
+        self.dlen = np.full(batch, d) if dlen is None else np.asarray(dlen)
+        self.u = rng.random((batch, rows)).astype(np.float32)
+
+
+@pytest.mark.parametrize("dt,batch,rows,vocab", [("f32", 9, 50, 151936), ("f32", 40, 256, 7001),
+                                                 ("bf16", 16, 64, 151936), ("f16", 64, 50, 50257),
+                                                 ("bf16", 300, 80, 6000), ("f32", 2, 40, 1 << 20)])
+def test_rows_on_the_path_alone(dt, batch, rows, vocab):
+    rng = np.random.default_rng(batch)
+    temp = rng.uniform(0.3, 1.4, batch)
+    temp[::3] = 0.0
+    c = Large(batch, rows, vocab, dt, seed=rows, temperature=temp, accept=0.95,
+              dlen=[rows - 1] + [int(x) for x in rng.integers(-1, rows, batch - 1)])
+    ctx = context(batch, rows, vocab)
+    try:
+        c.device()
+        for _ in range(2):
+            out = c.outputs()
+            c.call(ctx, out)
+            assert B.pld_sync(ctx) == B.PLD_OK, B.pld_last_error()
+            c.compare(out)
+    finally:
+        B.pld_destroy(ctx)
+
+
+@pytest.mark.parametrize("kind", ["chain", "star", "binary"])
+@pytest.mark.parametrize("temperature", [0.0, 0.8])
+def test_shapes_on_the_path_alone(kind, temperature):
+    c = Large(4, 256, 70001, seed=3, kind=kind, temperature=temperature, accept=0.98, pad=3,
+              offset=1)
+    ctx = context(4, 256, 70001)
+    try:
+        c.device()
+        out = c.outputs()
+        c.call(ctx, out)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        c.compare(out)
+    finally:
+        B.pld_destroy(ctx)
+
+
+def test_the_path_alone_twice_at_once_in_graphs_and_with_bad_requests():
+    """Two contexts' walks on two streams, more workgroups than the chip holds:
+    neither waits for the other. Then a graph of one, replayed."""
+    import torch
+    cases = [Large(24, 128, 50001, "bf16", seed=20 + i, accept=0.97) for i in range(2)]
+    ctxs = [context(24, 128, 50001) for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    try:
+        want = []
+        for c, ctx in zip(cases, ctxs):
+            c.parent[1, 5], c.u[2, 3], c.dlen[3] = 90, 1.5, 128
+            c.logits[4, 0, 77] = float("nan")
+            c.device()
+            want.append(c.outputs())
+            c.call(ctx, want[-1])
+            assert B.pld_sync(ctx) == B.PLD_EINVAL
+            c.compare(want[-1], skip=(1, 2, 3, 4))
+        torch.cuda.synchronize()
+        got = [[], []]
+        for _ in range(8):
+            for i, (c, ctx, st) in enumerate(zip(cases, ctxs, streams)):
+                with torch.cuda.stream(st):
+                    got[i].append(c.outputs())
+                    c.call(ctx, got[i][-1])
+        for i in range(2):
+            assert B.pld_sync(ctxs[i], streams[i]) == B.PLD_EINVAL
+            for out in got[i]:
+                for x, y in zip(out, want[i]):
+                    assert torch.equal(x, y)
+        c, ctx, out = cases[0], ctxs[0], cases[0].outputs()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[0]):
+            c.call(ctx, out)
+        rng = np.random.default_rng(9824)
+        for i in range(3):
+            c.u[5:] = rng.random((19, 128)).astype(np.float32)
+            c.d_u.copy_(torch.from_numpy(c.u))
+            for x in out:
+                x.fill_(-3)
+            graph.replay()
+            torch.cuda.synchronize()
+            c.compare(out, skip=(1, 2, 3, 4))
+    finally:
+        for ctx in ctxs:
+            B.pld_destroy(ctx)
 
 
 def check(*args, **kw):

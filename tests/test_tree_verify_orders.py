@@ -59,11 +59,11 @@ def compare(got, z64, draft, dlen, parent, u, temperature):
         assert (logp[b, n:] == 0).all()
 
 
-# (vocab, d) on both sides of what reads all rows (24 MiB of logits)
+@pytest.mark.parametrize("walk", [False, True])
 @pytest.mark.parametrize("dtype", [H.F32, H.F16, H.BF16])
 @pytest.mark.parametrize("batch,d,vocab", [(3, 0, 700), (2, 7, 1500), (3, 15, 2049), (2, 70, 301),
-                                           (1, 255, 130)])
-def test_all_rows(libs, dtype, batch, d, vocab):
+                                           (1, 255, 130), (2, 9, 9000)])
+def test_both_ways_to_read(libs, dtype, batch, d, vocab, walk):
     rng = np.random.default_rng([9601, dtype, d])
     parent = trees(rng, batch, d)
     temp = rng.uniform(0.4, 1.3, batch)
@@ -73,30 +73,15 @@ def test_all_rows(libs, dtype, batch, d, vocab):
     ctx = H.Context(libs[0], batch, d + 1, vocab)
     for order in H.ORDERS:
         got = T.verify(libs[1], ctx, raw, dtype, draft[:, :d], dlen, parent if d else None, u,
-                       temp, order)
+                       temp, order, walk)
         compare(got, z64, draft, dlen, parent, u, temp)
         assert ctx.clear()
 
 
-@pytest.mark.parametrize("dtype,batch,d,vocab", [(H.F32, 2, 31, 100003), (H.BF16, 1, 95, 132000),
-                                                 (H.F16, 2, 63, 100000)])
-def test_the_path_alone(libs, dtype, batch, d, vocab):
-    rng = np.random.default_rng([9602, dtype, d])
-    parent = trees(rng, batch, d)
-    temp = [0.9, 0.0][:batch]
-    raw, z64, draft, u = inputs(rng, batch, d, vocab, dtype, parent, temp)
-    u[0, :-1] *= 0.6
-    dlen = [d, d - 1][:batch]
-    ctx = H.Context(libs[0], batch, d + 1, vocab)
-    got = T.verify(libs[1], ctx, raw, dtype, draft, dlen, parent, u, temp,
-                   list(range(15, -1, -1)))
-    compare(got, z64, draft, dlen, parent, u, temp)
-    assert ctx.clear()
-
-
+@pytest.mark.parametrize("walk", [False, True])
 @pytest.mark.parametrize("kind", ["chain", "star", "comb", "binary"])
 @pytest.mark.parametrize("temperature", [0.0, 0.7])
-def test_tree_shapes(libs, kind, temperature):
+def test_tree_shapes(libs, kind, temperature, walk):
     rng = np.random.default_rng([9603, len(kind)])
     batch, d, vocab = 4, 20, 90
     parent = trees(rng, batch, d, kind)
@@ -104,7 +89,7 @@ def test_tree_shapes(libs, kind, temperature):
     raw, z64, draft, u = inputs(rng, batch, d, vocab, H.F32, parent, temp, 0.9)
     dlen = [d, d, 5, 0]
     ctx = H.Context(libs[0], batch, d + 1, vocab)
-    got = T.verify(libs[1], ctx, raw, H.F32, draft, dlen, parent, u, temp)
+    got = T.verify(libs[1], ctx, raw, H.F32, draft, dlen, parent, u, temp, walk=walk)
     compare(got, z64, draft, dlen, parent, u, temp)
 
 
@@ -138,7 +123,8 @@ def test_decisions_next_to_their_edge(libs):
         compare(got, z.astype(np.float64), draft, [d], parent, u, [1.0])
 
 
-def test_bad_requests_commit_nothing_and_are_flagged(libs):
+@pytest.mark.parametrize("walk", [False, True])
+def test_bad_requests_commit_nothing_and_are_flagged(libs, walk):
     rng = np.random.default_rng(9606)
     batch, d, vocab = 8, 6, 50
     parent = np.array([TR.random_tree(rng, d) for _ in range(batch)], np.int32)
@@ -155,7 +141,7 @@ def test_bad_requests_commit_nothing_and_are_flagged(libs):
     temp[6] = -1.0
     ctx = H.Context(libs[0], batch, d + 1, vocab)
     tok, path, acc, cnt, logp, err, broken = T.verify(libs[1], ctx, z, H.F32, draft, dlen, parent,
-                                                      u, temp)
+                                                      u, temp, walk=walk)
     assert err == H.BAD_BLOCK and broken == 0 and ctx.clear()
     assert (tok[:7] == -1).all() and (path[:7] == -1).all()
     assert (acc[:7] == 0).all() and (cnt[:7] == 0).all() and (logp[:7] == 0).all()
@@ -164,7 +150,8 @@ def test_bad_requests_commit_nothing_and_are_flagged(libs):
     parent[7, 3:] = 99
     draft[7, 3:] = -5
     dlen[:] = [-1] * 7 + [3]
-    got = T.verify(libs[1], ctx, z, H.F32, draft, dlen, parent, u, np.ones(batch))
+    got = T.verify(libs[1], ctx, z, H.F32, draft, dlen, parent, u, np.ones(batch), walk=walk)
+    assert ctx.clear()
     compare(got, z.astype(np.float64), draft, dlen, parent, u, np.ones(batch))
 
 
