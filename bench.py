@@ -224,6 +224,10 @@ def parse():
                     help="workload 5's start histories: time one verify step (the lookup "
                          "draft, the block's keys and values into a paged cache, attention "
                          "of the block, verification of the draft) instead of the drafting")
+    ap.add_argument("--tree-step", action="store_true",
+                    help="workload 5's start histories: time one verify step over trees (the "
+                         "lookup draft and three chains of a drafter's below the last token, "
+                         "head norms and cache append, attention, verification, kept cells)")
     ap.add_argument("--library-read", action="store_true",
                     help="also time torch.amax over the same rotated copies (a library "
                          "full read of the same bytes, for context)")
@@ -282,12 +286,13 @@ def main():
         print("--ngram drafts from the successor-count cache: it does not combine with "
               "--index or --fuse", file=sys.stderr)
         sys.exit(2)
-    if args.verify_step:
+    if args.verify_step or args.tree_step:
         if args.config != 5 or args.index or args.ngram or args.fuse != "none" or args.control \
                 or args.append_draft:
-            print("--verify-step: workload 5 with scan drafting only", file=sys.stderr)
+            print("--verify-step, --tree-step: workload 5 with scan drafting only",
+                  file=sys.stderr)
             sys.exit(2)
-        return bench_verify_step(args, torch, B, wl, dev)
+        return (bench_tree_step if args.tree_step else bench_verify_step)(args, torch, B, wl, dev)
     if args.config == 5:
         return bench_stream(args, torch, B, wl, dev)
 
@@ -1147,6 +1152,141 @@ def bench_verify_step(args, torch, B, wl, dev):
         "us_per_step": round(gpu_s * 1e6 / args.steps, 2),
         "us_per_call": {n: round(t, 2) for n, t in part.items()},
         "attend_cache_GBps": round(cache_bytes / part["attend"] / 1e3, 1),
+        "time_source": "value, ms_per_step: host clock around the replays, a device synchronize "
+                       "on each side; us_*: HIP events on the launch stream",
+    }
+    B.pld_destroy(ctx)
+    B.pld_destroy(target)
+    print(json.dumps(rec), flush=True)
+
+
+def bench_tree_step(args, torch, B, wl, dev):
+    """bench_verify_step over trees: below each history's last token stand its
+    lookup draft (16 tokens) and three chains of 5 random tokens, a drafter's
+    other guesses, in blocks of 32 rows. One layer's pld_kv_append_tree (with
+    head norms) and pld_attend_tree, pld_verify_tree on random logits that hold
+    the lookup draft at a probability of about 0.8, and pld_kv_keep of that
+    layer, captured into one graph and replayed."""
+    start = wl.config5_start(args.stream_start or wl.STREAM_START_LEN)
+    nb, k, other, chains = start.batch, start.k_max, 5, 3
+    rows = 1 + k + other * chains
+    hq, hk, dim, page, vocab = STEP_HEADS, STEP_KV_HEADS, STEP_DIM, STEP_PAGE, STEP_VOCAB
+    db = B.DeviceBatch(start.histories)
+    ctx = B.pld_create(nb, db.max_len)
+    p = B.pld_target_params_default()
+    p.max_batch, p.max_rows, p.max_len = nb, rows, db.max_len + rows - 1
+    p.q_heads, p.kv_heads, p.head_dim, p.page_tokens, p.vocab = hq, hk, dim, page, vocab
+    p.rope.rot_dim = dim
+    target = B.pld_create_target(p)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(12)
+    bf16, i32 = torch.bfloat16, torch.int32
+    width = -(-(db.max_len + rows - 1) // page)
+    pages = nb * width
+    table = torch.randperm(pages, generator=gen, device=dev).to(i32).view(nb, width)
+    kc = torch.empty((pages, hk, page, dim), dtype=bf16, device=dev)
+    vc = torch.empty((pages, hk, dim, page), dtype=bf16, device=dev)
+    for cells in (kc, vc):
+        for i in range(0, pages, 4096):
+            cells[i:i + 4096].normal_(generator=gen)
+    qkv = torch.randn((nb * rows, (hq + 2 * hk) * dim), generator=gen, device=dev).to(bf16)
+    q = torch.empty((nb * rows, hq * dim), dtype=bf16, device=dev)
+    norm = torch.ones(dim, device=dev)
+    attended = torch.zeros_like(q)
+    lookup, n1, match, _ = B.alloc_outputs(nb, k, device=dev)
+    guess = torch.randint(0, vocab, (nb, other * chains), generator=gen, device=dev, dtype=i32)
+    draft, parent = (torch.zeros((nb, rows - 1), dtype=i32, device=dev) for _ in range(2))
+    dlen = torch.zeros(nb, dtype=i32, device=dev)
+    uniform = torch.rand((nb, rows), generator=gen, device=dev)
+    tokens, path = (torch.empty((nb, rows), dtype=i32, device=dev) for _ in range(2))
+    accepted, counts = (torch.empty(nb, dtype=i32, device=dev) for _ in range(2))
+    logits = torch.empty((nb, rows, vocab), dtype=bf16, device=dev)
+    node = torch.arange(1, rows, dtype=i32, device=dev)[None, :]
+
+    def do_draft():
+        B.pld_draft_batch(ctx, db.rows, db.lengths, nb, start.n_min, start.n_max, k, lookup, n1,
+                          match)
+
+    def do_tree():
+        at = node - 1 - n1[:, None]  # of the other chains
+        first = lookup.gather(1, (node - 1).clamp(max=k - 1).long().expand(nb, -1))
+        second = guess.gather(1, at.clamp(0, other * chains - 1).long())
+        draft.copy_(torch.where(at < 0, first, second).clamp(min=0))
+        parent.copy_(torch.where((at >= 0) & (at % other == 0), 0, node - 1))
+        dlen.copy_(n1 + other * chains)
+
+    def do_append():
+        w = qkv.shape[1]
+        B.pld_kv_append_tree(target, qkv, w, qkv[:, hq * dim:], qkv[:, (hq + hk) * dim:], w, rows,
+                             db.lengths, dlen, parent, nb, table, width, kc, vc, pages, None, None,
+                             norm, norm, 1e-6, q)
+
+    def do_attend():
+        B.pld_attend_tree(target, q, hq * dim, rows, db.lengths, dlen, parent, 0, nb, table, width,
+                          kc, vc, pages, None, None, 0.0, 0, attended)
+
+    def do_verify():
+        B.pld_verify_tree(target, logits, vocab, rows, draft, dlen, parent, None, uniform, nb,
+                          tokens, path, accepted, counts)
+
+    def do_keep():
+        B.pld_kv_keep(target, db.lengths, dlen, path, accepted, rows, nb, table, width, kc, vc,
+                      pages)
+    do_draft()
+    do_tree()
+    for b in range(nb):
+        z = torch.randn((rows, vocab), generator=gen, device=dev) * 2.0
+        n = int(n1[b])
+        x = draft[b, :n].long()[:, None]
+        z[:n].scatter_(1, x, torch.logsumexp(z[:n], 1, keepdim=True) + 1.4)
+        logits[b] = z.to(bf16)
+    steps = {"draft": do_draft, "tree": do_tree, "kv_append_tree": do_append,
+             "attend_tree": do_attend, "verify_tree": do_verify, "kv_keep": do_keep}
+
+    def do_step():
+        for f in steps.values():
+            f()
+    do_step()
+    assert B.pld_sync(ctx) == B.PLD_OK and B.pld_sync(target) == B.PLD_OK
+    want = [t.clone() for t in (attended, tokens, path)]
+
+    def timed(f, reps, check):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            f()
+        for _ in range(max(1, args.warmup if reps == args.steps else 3)):
+            graph.replay()
+        torch.cuda.synchronize()
+        e0, e1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        t0 = time.perf_counter()
+        e0.record()
+        for _ in range(reps):
+            graph.replay()
+        e1.record()
+        torch.cuda.synchronize()
+        wall = time.perf_counter() - t0
+        for a_, b_ in zip(want, (attended, tokens, path)):
+            assert not check or torch.equal(a_, b_), "graph replay differs from the eager pass"
+        return wall, e0.elapsed_time(e1) * 1e-3
+    wall, gpu_s = timed(do_step, args.steps, True)
+    # (the cells that one call alone moves are not put back by the others)
+    part = {name: timed(f, min(200, args.steps), name != "attend_tree")[1]
+            / min(200, args.steps) * 1e6 for name, f in steps.items()}
+    assert B.pld_sync(ctx) == B.PLD_OK and B.pld_sync(target) == B.PLD_OK
+    rec = {
+        "metric": "tree verify steps/s; us per call of the step",
+        "value": round(args.steps / wall, 1), "unit": "verify steps/s", "n_gpus": 1,
+        "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(wall * 1e3 / args.steps, 6), "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": start.name, "batch": nb, "q_heads": hq, "kv_heads": hk,
+                   "head_dim": dim, "page_tokens": page, "vocab": vocab, "rows": rows,
+                   "layers": 1, "mean_nodes": round(float(dlen.float().mean()), 2),
+                   "mean_accepted": round(float(accepted.float().mean()), 2)},
+        "us_per_step": round(gpu_s * 1e6 / args.steps, 2),
+        "us_per_call": {n: round(t, 2) for n, t in part.items()},
+        "attend_TFLOPs": round(4.0 * float((dlen + 1).float().mean()) * nb * hq * dim
+                               * float(db.lengths.float().mean()) / part["attend_tree"] / 1e6, 1),
         "time_source": "value, ms_per_step: host clock around the replays, a device synchronize "
                        "on each side; us_*: HIP events on the launch stream",
     }
