@@ -18,7 +18,8 @@ constexpr int32_t kTreeRows = PLD_TREE_ROWS;
 PLD_INLINE int32_t parent_of(const int32_t *parent, const BlockArgs &g, int32_t b, int32_t t,
                              bool &stray)
 {
-    if (t < 1 || t > g.draft_len[b])
+    // (a draft length past the block is refused elsewhere: nothing is read for it)
+    if (t < 1 || t >= g.rows || t > g.draft_len[b])
         return 0;
     const int32_t p = parent ? parent[(int64_t)b * (g.rows - 1) + t - 1] : t - 1;
     if (p >= 0 && p < t)

@@ -765,6 +765,9 @@ hipError_t launch_typed(const TreeVerifyArgs &a, hipStream_t s)
     constexpr int kWide = 8192 / (16 / sizeof(T)) / kThreads;
     const int64_t rows = (int64_t)v.batch * v.rows, wide = pieces_of(v.vocab, 8192);
     const int64_t small = pieces_of(v.vocab, kMinPiece);
+    // (both launches or none: the second leaves the counters for the next call)
+    if (!fits_grid(v.batch * pieces_of(v.vocab, 8 * kThreads), kThreads))
+        return hipErrorInvalidConfiguration;
     hipError_t e;
     if (rows * v.vocab * (int64_t)sizeof(T) > kAllBytes)
         e = launch_walk<T, kWide>(a, sp, wide, s);

@@ -226,6 +226,26 @@ def test_a_bad_parent_stores_nothing_and_spares_the_others(rot, value):
         B.pld_destroy(ctx)
 
 
+@pytest.mark.parametrize("rot", [64, 20])
+@pytest.mark.parametrize("field,value,status", [("dl", 12, B.PLD_EINVAL),
+                                                ("dl", 2**31 - 1, B.PLD_EINVAL),
+                                                ("dl", -2, B.PLD_EINVAL),
+                                                ("ln", -1, B.PLD_EINVAL),
+                                                ("ln", 195, B.PLD_ECAPACITY)])
+def test_a_bad_block_stores_nothing(rot, field, value, status):
+    c = _batch()
+    ctx = context(3, 12, 200, 4, 2, 64, "bf16", "bf16", 16, rot)
+    try:
+        c[field][2] = value   # the last request: its tree ends the buffer
+        _call(ctx, **c)
+        assert B.pld_sync(ctx) == status
+        assert bool((c["out"][24:] == 0).all()) and not bool((c["out"][:12] == 0).any())
+        mine = c["tab"][2, :2].long()
+        assert bool((c["kc"][mine] == 0).all()) and bool((c["vc"][mine] == 0).all())
+    finally:
+        B.pld_destroy(ctx)
+
+
 def test_graph_replays_and_two_streams():
     import torch
     cases = [_batch(seed=1), _batch(seed=2)]

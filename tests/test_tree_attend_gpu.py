@@ -57,7 +57,7 @@ class Case(A.Case):
 
 def check(lengths, dlen, rows, kind=None, window=0, scale=0.0, max_len=0, **kw):
     c = Case(lengths, dlen, rows, kind, **kw)
-    ctx = c.context()
+    ctx = c.context(max(max_len, c.max_len))
     try:
         out, lse = c.outputs()
         c.call(ctx, out, lse, window, scale, max_len)
@@ -125,6 +125,13 @@ def test_idle_requests_strides_scales_and_a_loose_bound():
     check([100, 40], [3, 1], 4, max_len=103, seed=5)
     check([500, 33], [3, 0], 4, dim=128, peak=8.0, seed=1)
     check([500, 33], [3, 0], 4, dim=128, scale=-0.3, seed=3)
+    # 128 query rows a kv head, and of them 64 or fewer
+    for cache in ("bf16", "e4m3"):
+        check([500, 333, 70], [15, 7, 0], 16, dim=128, hq=16, hk=2, cache=cache, peak=8.0, seed=6)
+        check([500, 333, 70], [15, 7, 0], 16, dim=64, hq=16, hk=2, cache=cache, scale=-0.3, pad=8,
+              seed=7)
+        check([900, 333, 70], [15, 7, 0], 16, dim=128, hq=16, hk=2, cache=cache, max_len=70000,
+              page=128, seed=8)
 
 
 def test_chains_and_single_rows_are_the_chain_calls():

@@ -61,11 +61,9 @@ int main()
     int fails = 0;
     const int32_t values[] = {INT_MIN, -1, 0, 1, 2, 3, 4, 5, 254, 255, 256, INT_MAX};
     for (int32_t rows : {1, 2, 6, 256})
-        for (int32_t d : {-1, 0, 1, 5, 255})
+        for (int32_t d : {INT_MIN, -1, 0, 1, 5, 255, 256, INT_MAX})
             for (int32_t value : values)
                 for (int32_t t = -1; t < 260; ++t) {
-                    if (d >= rows)
-                        continue;
                     // exactly as long as the call says
                     std::unique_ptr<int32_t[]> p(new int32_t[2 * (rows - 1) + 1]);
                     for (int i = 0; i < 2 * (rows - 1); ++i)
@@ -76,7 +74,7 @@ int main()
                     a.draft_len = k.get();
                     bool stray = false;
                     const int32_t got = pld::parent_of(rows > 1 ? p.get() : nullptr, a, 1, t, stray);
-                    const bool node = t >= 1 && t <= d;
+                    const bool node = t >= 1 && t <= d && t < rows;
                     const bool fine = value >= 0 && value < t;
                     if (got != (node && fine ? value : 0) || stray != (node && !fine))
                         printf("%d %d %d %d\n", rows, d, value, t), ++fails;
