@@ -220,7 +220,9 @@ struct Branches {
 
 // Positions of a request's spans. A tree's are dealt out evenly: a batch with
 // ragged lengths has all of its workgroups at work, each on a share of its own
-// request, where equal spans leave the short requests' idle.
+// request, where equal spans leave the short requests' idle: 64 requests of
+// 8,192 to 65,536 positions, 96 query rows and 8-bit cells 1,155 us with equal
+// spans, 863 so.
 template <bool TREE, int GRAIN>
 __device__ __forceinline__ int32_t span_of(const Split &sp, const Sight &s)
 {

@@ -16,7 +16,9 @@ namespace {
 // down to 32 positions a query row: the partial results are 8 bytes a dim,
 // written and read, against 4 of cache. 16 x 262,144 positions, 128 rows:
 // 985 us with 2 MiB, 918 with 4 MiB; 32 x 16,384, 64 rows: 294 us with 64
-// positions a row, 236 with 32.
+// positions a row, 236 with 32. (attend_tall, which its products bound, takes 1 MiB:
+// the same within the spread from 512 KiB to 4 MiB with 16 bits a cell, and 1,155
+// us against 1,182 with 2 MiB for 64 ragged requests of 8-bit cells.)
 constexpr int64_t kFillGroups = 512;
 constexpr int64_t kEvenGroups = 1024;
 constexpr int64_t kMostGroups = 4096;
@@ -73,6 +75,12 @@ hipError_t launch_split(const AttendArgs &a, F kernel, hipStream_t s)
 // with 32): 16 rows 386, 546, 588; 17 rows 560, 548, 597; 64 rows 1,036, 573, 621;
 // 65 rows 1,268, 944, 621. 8-bit cells take the same rule; there narrow with 32
 // would hold out longer (head_dim 128, 64 rows: 144 against 168).
+//
+// Trees with more than 32 query rows take attend_tall where it has their head
+// size. Measured, wide and tall, requests of 65,536 positions and 2 kv heads of
+// 128: 44 rows, 16 requests, bf16 cells 223 and 221, 8-bit 184 and 153; 64 rows 240
+// and 231, 186 and 155; 68 rows 271 and 224; 128 rows 271 and 235, 263 and 227; 2
+// requests of 3,000 and 128 rows 27 and 25; 16 of 131,072 and 512 rows 1,602 and 1,300.
 template <typename T, typename C, int D, bool TREE>
 hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
 {
@@ -81,13 +89,15 @@ hipError_t launch_dim(const AttendArgs &a, hipStream_t s)
         return launch_split<Narrow<T, C, D, 1, TREE>, T, D>(a, attend_narrow<T, C, D, 1, TREE>, s);
     if constexpr (D <= 128)
         if (m <= 32)
-            return launch_split<Narrow<T, C, D, 2, TREE>, T, D>(a, attend_narrow<T, C, D, 2, TREE>, s);
-    if constexpr (TREE && (D == 64 || D == 128))
-        if (m > 64)
-            return launch_split<Tall<T, C, D>, T, D>(a, attend_tall<T, C, D>, s);
-    if (m <= 64)
-        return launch_split<Wide<T, C, D, 1, TREE>, T, D>(a, attend_wide<T, C, D, 1, TREE>, s);
-    return launch_split<Wide<T, C, D, 2, TREE>, T, D>(a, attend_wide<T, C, D, 2, TREE>, s);
+            return launch_split<Narrow<T, C, D, 2, TREE>, T, D>(a, attend_narrow<T, C, D, 2, TREE>,
+                                                                s);
+    if constexpr (TREE && (D == 64 || D == 128)) {
+        return launch_split<Tall<T, C, D>, T, D>(a, attend_tall<T, C, D>, s);
+    } else {
+        if (m <= 64)
+            return launch_split<Wide<T, C, D, 1, TREE>, T, D>(a, attend_wide<T, C, D, 1, TREE>, s);
+        return launch_split<Wide<T, C, D, 2, TREE>, T, D>(a, attend_wide<T, C, D, 2, TREE>, s);
+    }
 }
 
 template <typename T, typename C, bool TREE>

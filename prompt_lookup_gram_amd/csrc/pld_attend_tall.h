@@ -1,18 +1,33 @@
 // Attention of a tree's many rows over the paged cache, for gfx950 (MI355X):
-// more than 64 query rows a kv head.
+// more than 32 query rows a kv head.
 //
 // Mathematics as in pld_attend_device.h, in 32x32x16 matrix instructions: a
 // wavefront holds 32 query rows, a lane half of the positions of one of them.
-// With so many rows the matrix and vector units bound it, not the cache, so
-// what stands beside the products and the exponentials is kept small:
+// With so many rows the matrix and vector units bound it, not the cache: a score
+// costs 1/128 of a product's operands twice and one exponential. What was done
+// about it, and what it gave for 16 requests of 131,072 positions, 2 kv heads of 128
+// and 512 query rows (1.10 TFLOP; the 16x16 kernel of pld_attend_device.h: 1,602 us):
 //  - tiles of 64 positions, one barrier each; a tile goes into LDS row by row as it
-//    lies in memory (whole lines), the 16-byte chunks of a row exchanged so that
-//    eight neighbouring lanes read eight different bank groups;
-//  - 16-bit cells come by direct loads, whose addresses are a scalar's page and
-//    a lane's constant; 8-bit cells go through registers, where each is widened
-//    once for the workgroup;
-//  - masks, and positions that are not finite, are looked at in tiles where
-//    sights end only.
+//    lies in memory (whole lines), by direct loads whose addresses are a scalar's
+//    page and a lane's constants: 1,509;
+//  - the 16-byte chunks of a row exchanged so that 16 neighbouring lanes read all
+//    of the LDS's banks (half of its cycles were conflicts), and operands read two
+//    groups ahead of the product that takes them: 1,367;
+//  - the weights of one half of a tile worked out between the other half's
+//    products, masks kept to tiles where sights end: 1,350; a wavefront at its
+//    products before one at its weights: 1,300, 846 TFLOP/s, two thirds of what a
+//    large product reaches here.
+// Its fetches take a quarter of that (1,021 us with the first tiles read over and
+// over); the rest is the two units taking turns. The cache is read from HBM once:
+// 2.1 GB counted, the other three workgroups of a span find it in L2.
+// Tried and not kept: K fetched two tiles ahead, V one and a half (1,360); 8
+// wavefronts that share a tile (1,424: they wait for each other); 64 query rows a
+// wavefront, one a SIMD (2,540: its registers spill).
+//
+// 8-bit cells go through registers, where each is widened once for the workgroup:
+// 64 ragged requests of 8,192 to 65,536 positions, 4 kv heads of 128, up to 96 query
+// rows: 1,491 us when every wavefront widened for itself, 778 to 863 now, 2.8 to 3.1
+// TB/s; a span's start, its widening and its products follow each other there.
 #pragma once
 
 #include "pld_attend_device.h"
@@ -270,7 +285,8 @@ struct Tall : Tiles<T, C, D, 1, true> {
     }
 
     // HALVES: rows for two wavefronts only (a ragged tree): two take the first 32
-    // positions of a tile and two the others, and join at the end.
+    // positions of a tile and two the others, and join at the end. (A function of
+    // its own: with both in one the registers spill, 3,110 us against 1,150.)
     template <bool HALVES>
     static __device__ __forceinline__ void run(const AttendArgs &a, const Split &sp, char *lds,
                                                const Work &w)
