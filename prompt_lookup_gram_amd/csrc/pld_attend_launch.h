@@ -78,8 +78,10 @@ hipError_t launch_split(const AttendArgs &a, F kernel, hipStream_t s)
 //
 // Trees with more than 32 query rows take attend_tall where it has their head
 // size. Measured, wide and tall, requests of 65,536 positions and 2 kv heads of
-// 128: 44 rows, 16 requests, bf16 cells 223 and 221, 8-bit 184 and 153; 64 rows 240
-// and 231, 186 and 155; 68 rows 271 and 224; 128 rows 271 and 235, 263 and 227; 2
+// 128: 44 rows, 16 requests, 8-bit cells 180 to 185 and 153 to 159, bf16 the same
+// within the spread (223 to 228, 221 to 224); 64 rows 186 to 195 and 155 to 162,
+// bf16 again the same (wide spreads over 233 to 272, tall over 231 to 233); 68 rows,
+// bf16, 271 and 224; 128 rows 271 and 235, 8-bit 263 and 227; 2
 // requests of 3,000 and 128 rows 27 and 25; 16 of 131,072 and 512 rows 1,602 and 1,300.
 template <typename T, typename C, int D, bool TREE>
 hipError_t launch_dim(const AttendArgs &a, hipStream_t s)

@@ -19,7 +19,7 @@
 //    large product reaches here.
 // Its fetches take a quarter of that (1,021 us with the first tiles read over and
 // over); the rest is the two units taking turns. The cache is read from HBM once:
-// 2.1 GB counted, the other three workgroups of a span find it in L2.
+// 2.17 GB counted, the other three workgroups of a span find it in L2.
 // Tried and not kept: K fetched two tiles ahead, V one and a half (1,360); 8
 // wavefronts that share a tile (1,424: they wait for each other); 64 query rows a
 // wavefront, one a SIMD (2,540: its registers spill).

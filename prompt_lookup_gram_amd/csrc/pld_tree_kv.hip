@@ -343,8 +343,8 @@ hipError_t launch_cells(const TreeAppendArgs &ta, hipStream_t s)
 // same line.
 // Bound by V's lines: a moved cell is 2 bytes of a 128-byte line in every dim. 64
 // requests, 32 layers, 8 kv heads of 128, paths of up to 8 nodes: 118 us, 148 when
-// the cache was not just used, for 326 MB read and 76 MB written where the moved
-// cells are 67 MB. K alone 14 us, V's stores 18 more, its loads 58. Non-temporal
+// the cache was not just used, for 334 MB read and 78 MB written where the moved
+// cells are 67 MB. K alone 14 us, with V's stores 33, with V's loads 73. Non-temporal
 // loads: 128; stores too: 153.
 template <typename C, int D>
 __global__ __launch_bounds__(kThreads) void keep_cells(KeepArgs a, int64_t units)

@@ -363,7 +363,7 @@ constexpr int32_t kDone = 1 << 16;  // `arrived` counts pieces taken below, piec
 // waits for that. It waits for workgroups that run and wait for nothing
 // themselves while they have a piece: the walk ends however many of a team the
 // chip has room for, one included. 64 trees of up to 64 rows of 151,936 bf16 logits:
-// 58 us, 46 MB read, 6 to 7 us a row of the longest path: taking a piece, reading,
+// 58 us, 47 MB read, 6 to 7 us a row of the longest path: taking a piece, reading,
 // counting in, joining and being seen are a round trip each. (One workgroup of 1,024
 // threads a request: 97, its exponentials bound it.)
 template <typename T, int W>
