@@ -157,9 +157,9 @@ struct Tall : Tiles<T, C, D, 1, true> {
         if constexpr (kLoads == 4)
             asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %6\n\ts_nop 0\n\t"
                          "global_load_lds_dwordx4 %1, %5\n\t"
-                         "global_load_lds_dwordx4 %2, %5 offset:1024\n\t"
-                         "global_load_lds_dwordx4 %3, %5 offset:2048\n\t"
-                         "global_load_lds_dwordx4 %4, %5 offset:3072\n\ts_mov_b32 m0, %0"
+                         "global_load_lds_dwordx4 %2, %5 offset:1*1024\n\t"
+                         "global_load_lds_dwordx4 %3, %5 offset:2*1024\n\t"
+                         "global_load_lds_dwordx4 %4, %5 offset:3*1024\n\ts_mov_b32 m0, %0"
                          : "=&s"(m0)
                          : "v"(x.k_off[0]), "v"(x.k_off[1]), "v"(x.k_off[2]), "v"(x.k_off[3]),
                            "s"(k), "s"(k_to)
@@ -167,7 +167,7 @@ struct Tall : Tiles<T, C, D, 1, true> {
         else
             asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %4\n\ts_nop 0\n\t"
                          "global_load_lds_dwordx4 %1, %3\n\t"
-                         "global_load_lds_dwordx4 %2, %3 offset:1024\n\ts_mov_b32 m0, %0"
+                         "global_load_lds_dwordx4 %2, %3 offset:1*1024\n\ts_mov_b32 m0, %0"
                          : "=&s"(m0)
                          : "v"(x.k_off[0]), "v"(x.k_off[1]), "s"(k), "s"(k_to)
                          : "memory");

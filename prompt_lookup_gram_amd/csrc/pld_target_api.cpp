@@ -1,7 +1,7 @@
 // C-ABI entry points of the verify step (include/pld.h): the target context,
 // argument checks and the launches of pld_kv.hip, pld_attend.hip,
-// pld_verify.hip and their counterparts for trees. No compute happens here but the rotary frequencies, once
-// per context.
+// pld_verify.hip and their counterparts for trees. No compute happens here but
+// the rotary frequencies, once per context.
 
 #include <math.h>
 #include <stdint.h>

@@ -287,6 +287,32 @@ def test_repeated_calls_are_bit_identical_and_graphs_replay():
         B.pld_destroy(ctx)
 
 
+@pytest.mark.parametrize("rows", [3, 7, 12, 40])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("longest", [60, 3000])
+def test_out_in_qs_place(rows, cache, longest):
+    # 12, 28, 48 and 160 query rows a kv head, one span and several
+    import torch
+    c = Case([longest, 40, 0], [rows - 1, 2, 1], rows, hq=8, hk=2, dim=128, cache=cache, page=32,
+             seed=rows)
+    ctx = c.context()
+    try:
+        want, lse = c.outputs()
+        c.call(ctx, want, lse)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        c.compare(want, lse)
+        q = c.q.clone()
+        _, again = c.outputs()
+        c.again(ctx, c.q, again)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        assert torch.equal(lse, again)
+        live = (lse[:, :, :1] != 7.0).unsqueeze(-1)
+        # (padded rows keep q's values)
+        assert torch.equal(c.q.view_as(want), torch.where(live, want, q.view_as(want)))
+    finally:
+        B.pld_destroy(ctx)
+
+
 def test_two_contexts_on_two_streams_at_once():
     import torch
     cases = [Case([6000, 300], [15, 3], 16, hq=8, hk=2, dim=128, page=64, seed=15),

@@ -267,6 +267,28 @@ def test_strides_and_alignments(pad, offset, dt, vocab):
     check(2, 60, vocab, dt, seed=pad, pad=pad, offset=offset, temperature=0.8)
 
 
+@pytest.mark.parametrize("cls,batch,rows,vocab", [(Case, 3, 20, 9000), (Large, 40, 256, 7001)])
+def test_no_temperature_and_no_log_probabilities(cls, batch, rows, vocab):
+    # (no temperature is 1, and no buffer for the log probabilities is none written)
+    import torch
+    c = cls(batch, rows, vocab, seed=29)
+    ctx = context(batch, rows, vocab)
+    try:
+        c.device()
+        want, out = c.outputs(), c.outputs()
+        c.call(ctx, want)
+        c.d_temp = None
+        c.call(ctx, (*out[:4], None))
+        assert B.pld_sync(ctx) == B.PLD_OK
+        c.compare(want)
+        assert all(torch.equal(x, y) for x, y in zip(out[:4], want))
+        c.call(ctx, out)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        assert torch.equal(out[4], want[4])
+    finally:
+        B.pld_destroy(ctx)
+
+
 def test_ties_and_peaked_and_flat_rows():
     check(6, 20, 3000, "bf16", seed=1, temperature=0.0, ties=True)
     check(6, 20, 3000, seed=2, temperature=0.05, spread=6.0)
