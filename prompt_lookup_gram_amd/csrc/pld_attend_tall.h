@@ -230,10 +230,11 @@ struct Tall : Tiles<T, C, D, 1, true> {
     }
 
     // A tile where a sight ends: V of positions past the span's end becomes
-    // zero, and so does V of a position with an infinity or a NaN (0 times it
-    // would be NaN in the rows that do not see it); returns such positions,
-    // whose share the rows that see them then add. Barriers stand before and
-    // behind it.
+    // zero, and so does each element that is an infinity or a NaN (0 times it
+    // would be NaN in the rows that do not see it); returns the positions that
+    // hold such elements, which the rows that see them then add. The other
+    // elements of such a position stay, for the products. Barriers stand before
+    // and behind it.
     static __device__ __forceinline__ uint64_t clean(char *stage, uint32_t *odd, int32_t last)
     {
         constexpr uint32_t kExp = __is_same(T, __bf16) ? 0x7f80u : 0x7c00u;
@@ -571,7 +572,8 @@ struct Tall : Tiles<T, C, D, 1, true> {
                 sums(2);
                 sums(3);
             }
-            // positions that are not finite, for the rows that see them
+            // elements that are not finite, for the rows that see them (no weight
+            // changes what they make of a sum, so an older maximum's will do)
             if (HALVES)  // (those of its half)
                 odd &= mine ? ~0ull << 32 : 0xffffffffull;
             for (; odd; odd &= odd - 1) {
@@ -595,8 +597,12 @@ struct Tall : Tiles<T, C, D, 1, true> {
 #pragma unroll
                 for (int k = 0; k < DB; ++k)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[k][e] += p * to_f32(from[(k * 32 + (e >> 2) * 8 + (e & 3)) * x.tokens]);
+                    for (int e = 0; e < 16; ++e) {
+                        const float y =
+                            to_f32(from[(k * 32 + (e >> 2) * 8 + (e & 3)) * x.tokens]);
+                        if (!__builtin_isfinite(y))
+                            o[k][e] += p * y;
+                    }
             }
             if constexpr (kByte) {
                 if (i + 1 < tiles) {
