@@ -467,7 +467,7 @@ struct Tiles {
                                                 const int32_t (&low)[MB], const C *vc, int32_t b,
                                                 int32_t j0, int32_t s1, const BlockArgs &g,
                                                 int32_t h, int lane, const char *branches,
-                                                int32_t root)
+                                                bool branchy, int32_t root)
     {
         const int grp = lane >> 4;
         const int32_t left = s1 - (j0 + grp * CH);  // slots 0..left are in the span
@@ -513,9 +513,11 @@ struct Tiles {
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb) {
                     const float w = to_f32((T)__shfl(st[mb][e / 4][e % 4], from * 16 + (lane & 15)));
-                    // (a tree's rows: pos is their node)
-                    const bool sees = TREE ? Branches::bits(branches, pos[mb], j, root) & 1
-                                           : j <= pos[mb];
+                    // (a tree's rows: pos is their node. Without branches nothing
+                    // lies behind the root.)
+                    const bool sees =
+                        TREE ? !branchy || (Branches::bits(branches, pos[mb], j, root) & 1)
+                             : j <= pos[mb];
                     if (sees && j >= low[mb]) {
 #pragma unroll
                         for (int i = 0; i < DB; ++i)
@@ -776,7 +778,8 @@ struct Narrow : Tiles<T, C, D, MB, TREE> {
                               ? Branches::bits(branches, pos[mb], j0 + grp * CH, root)
                               : 0xffffffffu);
             if (edge)
-                S::hide(v, o, st, pos, low, vc, w.b, j0, w.s1, g, w.h, lane, branches, root);
+                S::hide(v, o, st, pos, low, vc, w.b, j0, w.s1, g, w.h, lane, branches, branchy,
+                        root);
 #pragma unroll
             for (int i = 0; i < DB; ++i)
 #pragma unroll
@@ -1015,7 +1018,8 @@ struct Wide : Tiles<T, C, D, RB, TREE> {
             for (int n = 0; n < DB; ++n)
                 v[n] = x[(FK + n) * kWave];
             if (edge)
-                S::hide(v, o, st, pos, low, vc, w.b, j0, w.s1, g, w.h, lane, branches, root);
+                S::hide(v, o, st, pos, low, vc, w.b, j0, w.s1, g, w.h, lane, branches, branchy,
+                        root);
 #pragma unroll
             for (int n = 0; n < DB; ++n)
 #pragma unroll

@@ -94,3 +94,29 @@ def test_other_dims_do_not_feel_a_value_that_is_not_finite(dt, cache, value, dim
             check_hits(c, out, lse, hits, value, window)
     finally:
         B.pld_destroy(ctx)
+
+
+# narrow (8 and 24 query rows), wide and many-row kernels
+@pytest.mark.parametrize("hq,rows,dim", [(2, 4, 64), (2, 12, 128), (8, 12, 96), (8, 12, 128)])
+@pytest.mark.parametrize("back", [0, 1, 31, 32])
+def test_a_root_alone_sees_its_own_last_positions(hq, rows, dim, back):
+    """A request without drafts in a batch of trees has no branches to look at:
+    what a workgroup before it left behind says nothing about what it sees."""
+    quiet = Case([40] * 600, [0] * 600, rows, hq=hq, hk=1, dim=dim, seed=22)
+    quiet.vc.zero_()
+    c = Case([70, 64, 33, 41], [0, 0, 0, rows - 1], rows, hq=hq, hk=1, dim=dim, seed=23)
+    hits = [(i, c.lengths[i] - 1 - back, 0, 7 + i) for i in range(4)]
+    for i, p, head, d in hits:
+        put(c, i, p, head, d, float("inf"))
+    first, ctx = quiet.context(), c.context()
+    try:
+        out, lse = quiet.outputs()
+        quiet.call(first, out, lse)
+        assert B.pld_sync(first) == B.PLD_OK
+        out, lse = c.outputs()
+        c.call(ctx, out, lse)
+        assert B.pld_sync(ctx) == B.PLD_OK
+        check_hits(c, out, lse, hits, "inf", 0)
+    finally:
+        B.pld_destroy(first)
+        B.pld_destroy(ctx)
