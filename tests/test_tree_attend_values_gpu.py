@@ -7,6 +7,7 @@ that sees it is that infinity, or NaN; every other dim is as if it were not ther
 
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
 import target_reference as R
@@ -119,4 +120,54 @@ def test_a_root_alone_sees_its_own_last_positions(hq, rows, dim, back):
         check_hits(c, out, lse, hits, "inf", 0)
     finally:
         B.pld_destroy(first)
+        B.pld_destroy(ctx)
+
+
+@pytest.mark.parametrize("hq", [16, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page,first", [(16, 80), (16, 64), (64, 64), (128, 128)])
+def test_a_page_that_the_window_left_behind_is_not_needed_by_many_rows(hq, dim, cache, page, first):
+    # (64 and 160 query rows a kv head: the many-row kernel has its own fetch)
+    c = Case([200], [3], 4, "star", hq=hq, hk=1, dim=dim, cache=cache, page=page, seed=24)
+    ctx = c.context()
+    try:
+        table = c.table.copy()
+        table[0, :first // page] = -1
+        out, lse = c.outputs()
+        c.call(ctx, out, lse, window=200 - first, table=table)  # the root sees from `first` on
+        assert B.pld_sync(ctx) == B.PLD_OK
+        c.compare(out, lse, window=200 - first)
+        c.call(ctx, out, lse, window=201 - first, table=table)
+        assert B.pld_sync(ctx) == B.PLD_EINVAL
+        assert bool(out[0, 0].isnan().all())
+    finally:
+        B.pld_destroy(ctx)
+
+
+@pytest.mark.parametrize("hq,hk,dim,dt,cache", [(4, 2, 128, "bf16", "bf16"),
+                                                (8, 2, 128, "f16", "e4m3"),
+                                                (16, 1, 128, "bf16", "bf16"),
+                                                (16, 1, 64, "f16", "e4m3"),
+                                                (8, 1, 96, "bf16", "bf16")])
+def test_ragged_batches_repeat_themselves_bit_for_bit(hq, hk, dim, dt, cache):
+    """Another call between them, and the spans' partial results of another
+    batch in the workspace, change nothing."""
+    import torch
+    rng = np.random.default_rng(9703)
+    lengths = [int(n) for n in rng.integers(1, 9000, 12)]
+    dlen = [int(n) for n in rng.integers(0, 12, 12)]
+    c = Case(lengths, dlen, 12, hq=hq, hk=hk, dim=dim, dt=dt, cache=cache, page=64, seed=25)
+    ctx = c.context()
+    try:
+        want = c.outputs()
+        c.call(ctx, *want)
+        for _ in range(6):
+            other = c.outputs()
+            c.again(ctx, *other, window=700)
+            out, lse = c.outputs()
+            c.again(ctx, out, lse)
+            assert B.pld_sync(ctx) == B.PLD_OK
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    finally:
         B.pld_destroy(ctx)
