@@ -15,8 +15,8 @@
 //    groups ahead of the product that takes them: 1,367;
 //  - the weights of one half of a tile worked out between the other half's
 //    products, masks kept to tiles where sights end: 1,350; a wavefront at its
-//    products before one at its weights: 1,300, 846 TFLOP/s, two thirds of what a
-//    large product reaches here.
+//    products before one at its weights: 1,300 to 1,335, 824 to 846 TFLOP/s, three
+//    fifths of what a large product reaches here.
 // Its fetches take a quarter of that (1,021 us with the first tiles read over and
 // over); the rest is the two units taking turns. The cache is read from HBM once:
 // 2.17 GB counted, the other three workgroups of a span find it in L2.
@@ -26,7 +26,7 @@
 //
 // 8-bit cells go through registers, where each is widened once for the workgroup:
 // 64 ragged requests of 8,192 to 65,536 positions, 4 kv heads of 128, up to 96 query
-// rows: 1,491 us when every wavefront widened for itself, 778 to 863 now, 2.8 to 3.1
+// rows: 1,491 us when every wavefront widened for itself, 752 to 863 now, 2.8 to 3.2
 // TB/s; a span's start, its widening and its products follow each other there.
 #pragma once
 

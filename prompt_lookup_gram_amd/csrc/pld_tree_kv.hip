@@ -13,8 +13,9 @@
 // heads, 16 elements a lane (with the half layout a word and its partner in
 // the pair), so that a head is a few lanes side by side, its sum a few
 // exchanges, and no barrier stands anywhere. V is stored as in pld_kv.hip.
-// 50,001 rows of 32 + 8 + 8 heads of 128 in bf16: 257 to 265 us, 4.6 to 4.8 TB/s
-// read and written, the rate of a large copy. 64 trees of up to 64 rows: 20 us for
+// 50,001 rows of 32 + 8 + 8 heads of 128 in bf16: 257 to 265 us back to back (265
+// to 296 launch by launch under the trace), 4.6 to 4.8 TB/s read and written; a
+// large copy reaches 4.5 to 5.0. 64 trees of up to 64 rows: 20 us for
 // 51 MB; one tree of 16 rows 7.8, the chain of lengths, words, angles and stores.
 // Two heads ahead instead of one: 23 and 277 us.
 
@@ -342,8 +343,8 @@ hipError_t launch_cells(const TreeAppendArgs &ta, hipStream_t s)
 // side by side, kBatch moves of a dim are neighbouring lanes: they touch the
 // same line.
 // Bound by V's lines: a moved cell is 2 bytes of a 128-byte line in every dim. 64
-// requests, 32 layers, 8 kv heads of 128, paths of up to 8 nodes: 118 us, 148 when
-// the cache was not just used, for 334 MB read and 78 MB written where the moved
+// requests, 32 layers, 8 kv heads of 128, paths of up to 8 nodes: 118 us, 142 to 154
+// when the cache was not just used, for 334 MB read and 78 MB written where the moved
 // cells are 67 MB. K alone 14 us, with V's stores 33, with V's loads 73. Non-temporal
 // loads: 128; stores too: 153.
 template <typename C, int D>

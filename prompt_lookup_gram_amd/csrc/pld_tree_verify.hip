@@ -750,6 +750,9 @@ hipError_t launch_draw(const TreeVerifyArgs &a, const Space &sp, hipStream_t s)
 // bf16 logits 22 us (the same call), 4 trees 28 and 42, 8 (155 MB) 50 and 51, 16 (311
 // MB) 70 and 71, 24 80 and 61, 64 239 and 87; 64 of 16 rows (311 MB) 77 and 97; 64 of 32
 // rows of 50,257 (206 MB) 62 and 64; 16 full ones of those (51 MB, greedy) 27 and 62.
+// Bytes alone do not place every shape: the path costs a round trip a level and all
+// rows cost their live bytes, so many trees of few rows just past the bound take the
+// slower side (97 for 77).
 constexpr int64_t kAllBytes = 256 << 20;
 constexpr int64_t kResident = 2048;      // workgroups of a walk that the chip holds at once
 
